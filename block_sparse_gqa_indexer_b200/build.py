@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libs5attn.so")
 SOURCES = ["api.cu", "index_topk.cu", "index_gemm.cu", "attn_decode.cu", "attn_tile.cu", "index_noalloc.cu",
-           "kv_append.cu"]
+           "kv_append.cu", "attn_dense.cu", "batch_build.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -476,6 +476,63 @@ s5_status workspace_need(const s5_batch_desc *batch, int32_t window, int groups,
   return S5_OK;
 }
 
+// ---- dense attention over the whole cache ----
+
+struct DenseWs {
+  size_t part_o, part_ml, end;
+  int n_split;
+};
+
+DenseWs dense_ws(const s5_batch_desc *b) {
+  DenseWs w{};
+  const long long units = (long long)b->total_q * kKv;
+  w.n_split = units > 0 ? (int)(592 / units) : 1;
+  w.n_split = w.n_split < 1 ? 1 : (w.n_split > 32 ? 32 : w.n_split);
+  w.part_o = kWsFixed;
+  w.part_ml = align_up(w.part_o + (size_t)b->total_q * kHeads * w.n_split * kD * sizeof(float), 256);
+  w.end = align_up(w.part_ml + (size_t)b->total_q * kHeads * w.n_split * 2 * sizeof(float), 256);
+  return w;
+}
+
+// kv8 as in attn_common.
+s5_status dense_common(const s5_kv_desc *kv, const s5_batch_desc *b, const void *q, float sm_scale, void *out, float *lse,
+                       void *ws, size_t ws_bytes, cudaStream_t stream, bool kv8, float k_scale, float v_scale) {
+  s5_status st = check_batch(b);
+  if (st != S5_OK) return st;
+  if ((st = check_kv(kv)) != S5_OK) return st;
+  if (!std::isfinite(sm_scale)) return S5_ERR_INVALID_ARG;
+  if (kv8 && (!std::isfinite(k_scale) || !std::isfinite(v_scale) || !std::isfinite(sm_scale * k_scale)))
+    return S5_ERR_INVALID_ARG;
+  if (ws == nullptr) return S5_ERR_WORKSPACE;
+  if (b->total_q == 0) return S5_OK;
+  if (q == nullptr || out == nullptr || !aligned16(q) || !aligned16(out)) return S5_ERR_INVALID_ARG;
+  const DenseWs w = dense_ws(b);
+  if (ws_bytes < w.end) return S5_ERR_WORKSPACE;
+  uint8_t *wsb = static_cast<uint8_t *>(ws);
+  DenseArgs a{};
+  a.k_pool = kv->k_pool;
+  a.v_pool = kv->v_pool;
+  a.num_pages = kv->num_pages;
+  a.q = q;
+  a.page_table = b->page_table;
+  a.max_pages = b->max_pages;
+  a.ctx_lens = b->ctx_lens;
+  a.cu_q = b->cu_q;
+  a.batch = b->batch;
+  a.total_q = b->total_q;
+  a.max_len = b->max_len;
+  a.scale_log2 = (kv8 ? sm_scale * k_scale : sm_scale) * 1.4426950408889634f;
+  a.v_scale = kv8 ? v_scale : 1.f;
+  a.kv8 = kv8 ? 1 : 0;
+  a.n_split = w.n_split;
+  a.out = out;
+  a.lse = lse;
+  a.part_o = reinterpret_cast<float *>(wsb + w.part_o);
+  a.part_ml = reinterpret_cast<float *>(wsb + w.part_ml);
+  a.err = reinterpret_cast<int32_t *>(ws);
+  return cuda_status(launch_dense(a, stream));
+}
+
 // Block scores and top-k for `groups` indexer queries per token: q_index
 // [total_q][groups][256], one selection per (token, group) row.
 s5_status index_common(const s5_index_desc *index, const s5_batch_desc *batch, const void *q_index, int32_t topk,
@@ -641,6 +698,27 @@ s5_status s5_swa_gqa_attn(const s5_kv_desc *kv, const s5_batch_desc *batch, cons
                           s5_stream_t stream) {
   return attn_common(kModeSwa, kv, batch, q, nullptr, nullptr, 0, window, sm_scale, out, lse, workspace,
                      workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+s5_status s5_workspace_size_dense(const s5_batch_desc *batch, int32_t window, size_t *bytes) {
+  const s5_status st = workspace_need(batch, window, 1, bytes);
+  if (st != S5_OK) return st;
+  const size_t dense = dense_ws(batch).end;
+  if (dense > *bytes) *bytes = dense;
+  return S5_OK;
+}
+
+s5_status s5_dense_gqa_attn(const s5_kv_desc *kv, const s5_batch_desc *batch, const void *q, float sm_scale, void *out,
+                            float *lse, void *workspace, size_t workspace_bytes, s5_stream_t stream) {
+  return dense_common(kv, batch, q, sm_scale, out, lse, workspace, workspace_bytes,
+                      reinterpret_cast<cudaStream_t>(stream), false, 1.f, 1.f);
+}
+
+s5_status s5_dense_gqa_attn_fp8kv(const s5_kv_desc *kv, const s5_batch_desc *batch, const void *q, float sm_scale,
+                                  float k_scale, float v_scale, void *out, float *lse, void *workspace,
+                                  size_t workspace_bytes, s5_stream_t stream) {
+  return dense_common(kv, batch, q, sm_scale, out, lse, workspace, workspace_bytes,
+                      reinterpret_cast<cudaStream_t>(stream), true, k_scale, v_scale);
 }
 
 s5_status s5_reset_device_error(void *workspace, s5_stream_t stream) {

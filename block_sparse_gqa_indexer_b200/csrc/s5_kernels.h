@@ -142,6 +142,30 @@ struct TileArgs {
   int32_t *err;
 };
 
+// Dense attention over the whole cache.
+struct DenseArgs {
+  const void *k_pool, *v_pool;
+  int num_pages;
+  const void *q;
+  const int32_t *page_table;
+  int max_pages;
+  const int32_t *ctx_lens;
+  const int32_t *cu_q;
+  int batch;
+  int total_q;
+  int max_len;
+  float scale_log2;  // sm_scale * log2(e) (one-byte KV: times k_scale)
+  float v_scale;     // one-byte KV: value of a V code = v_scale * E4M3(code)
+  int kv8;           // nonzero: K / V pools hold one-byte E4M3 codes
+  int n_split;
+  void *out;
+  float *lse;
+  float *part_o;
+  float *part_ml;
+  int32_t *err;
+};
+cudaError_t launch_dense(const DenseArgs &a, cudaStream_t st);
+
 // cudaFuncSetAttribute(kernel, MaxDynamicSharedMemorySize, bytes) on the
 // current device, skipped when an equal or larger value is already set there
 // (the host cost of a call stays off the launch path of small batches).

@@ -21,7 +21,7 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python -m block_sparse_gqa_indexer_b200.build`")
 _lib = ctypes.CDLL(LIB_PATH)
 
-ABI_VERSION = 102  # S5_ABI_VERSION of the header this binding follows
+ABI_VERSION = 103  # S5_ABI_VERSION of the header this binding follows
 N_HEADS, N_KV, HEAD_DIM, PAGE, BLOCK, INDEX_DIM, MAX_TOPK = 64, 4, 192, 64, 8, 256, 512
 MAX_LEN = 1 << 21
 DEFAULT_SM_SCALE = 1.0 / math.sqrt(HEAD_DIM)
@@ -36,6 +36,7 @@ SYMBOLS = ("s5_workspace_size", "s5_index_score_topk", "s5_sparse_gqa_attn", "s5
            "s5_index_score_topk_fp8", "s5_sparse_gqa_attn_fp8kv",
            "s5_workspace_size_grouped", "s5_index_score_topk_grouped", "s5_sparse_gqa_attn_grouped",
            "s5_index_score_topk_noalloc", "s5_append_kv", "s5_append_kv_fp8", "s5_reset_device_error", "s5_get_device_error",
+           "s5_workspace_size_dense", "s5_dense_gqa_attn", "s5_dense_gqa_attn_fp8kv", "s5_build_batch",
            "s5_status_string", "s5_abi_version")
 
 
@@ -52,6 +53,11 @@ class BatchDesc(ctypes.Structure):
     _fields_ = [("page_table", ctypes.c_void_p), ("ctx_lens", ctypes.c_void_p), ("cu_q", ctypes.c_void_p),
                 ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("total_q", ctypes.c_int32),
                 ("max_q", ctypes.c_int32), ("max_len", ctypes.c_int32)]
+
+
+class RequestDesc(ctypes.Structure):
+    _fields_ = [("req_pages", ctypes.c_void_p), ("free_pages", ctypes.c_void_p), ("num_reqs", ctypes.c_int32),
+                ("req_stride", ctypes.c_int32), ("num_free", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -76,6 +82,13 @@ _lib.s5_append_kv.argtypes = [ctypes.POINTER(KvDesc), ctypes.POINTER(IndexDesc),
                               _P, _P, ctypes.c_size_t, _P]
 _lib.s5_append_kv_fp8.argtypes = [ctypes.POINTER(KvDesc), ctypes.POINTER(IndexDesc), ctypes.POINTER(BatchDesc), _P,
                                   _P, _P, ctypes.c_float, ctypes.c_float, _P, ctypes.c_size_t, _P]
+_lib.s5_workspace_size_dense.argtypes = _lib.s5_workspace_size.argtypes
+_lib.s5_dense_gqa_attn.argtypes = [ctypes.POINTER(KvDesc), ctypes.POINTER(BatchDesc), _P, ctypes.c_float, _P, _P, _P,
+                                   ctypes.c_size_t, _P]
+_lib.s5_dense_gqa_attn_fp8kv.argtypes = [ctypes.POINTER(KvDesc), ctypes.POINTER(BatchDesc), _P, ctypes.c_float,
+                                         ctypes.c_float, ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P]
+_lib.s5_build_batch.argtypes = [ctypes.POINTER(RequestDesc), _P, _P, ctypes.POINTER(BatchDesc), _P, _P, _P, _P,
+                                ctypes.c_size_t, _P]
 _lib.s5_reset_device_error.argtypes = [_P, _P]
 _lib.s5_get_device_error.argtypes = [_P, _P, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]
 _lib.s5_status_string.argtypes = [ctypes.c_int]
@@ -168,10 +181,21 @@ def s5_workspace_size_grouped(batch: Batch, window: int = 0) -> int:
     return int(n.value)
 
 
-def new_workspace(batch: Batch, window: int = 0, device="cuda", grouped: bool = False) -> torch.Tensor:
+def s5_workspace_size_dense(batch: Batch, window: int = 0) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.s5_workspace_size_dense(ctypes.byref(batch.desc), int(window), ctypes.byref(n)),
+           "s5_workspace_size_dense")
+    return int(n.value)
+
+
+def new_workspace(batch: Batch, window: int = 0, device="cuda", grouped: bool = False,
+                  dense: bool = False) -> torch.Tensor:
     """Allocate (with torch) and zero a workspace sized for ``batch`` (with
-    ``grouped``, also for the per-KV-group selection calls)."""
+    ``grouped``, also for the per-KV-group selection calls; with ``dense``,
+    also for dense attention)."""
     n = s5_workspace_size_grouped(batch, window) if grouped else s5_workspace_size(batch, window)
+    if dense:
+        n = max(n, s5_workspace_size_dense(batch, window))
     return torch.zeros(max(256, n), dtype=torch.uint8, device=device)
 
 
@@ -343,6 +367,66 @@ def s5_append_kv_fp8(k_pool, v_pool, key_pool, batch: Batch, k_new, v_new, key_n
                                  ctypes.byref(batch.desc), _ptr(k_new), _ptr(v_new),
                                  None if idx is None else _ptr(key_new), float(k_scale), float(v_scale), _ptr(ws),
                                  ws.numel(), _stream(stream)), "s5_append_kv_fp8")
+
+
+def _dense_args(batch: Batch, q, out, lse, ws):
+    _need(q, torch.bfloat16, "q", (batch.total_q, N_HEADS, HEAD_DIM))
+    _need(out, torch.bfloat16, "out", (batch.total_q, N_HEADS, HEAD_DIM))
+    if lse is not None:
+        _need(lse, torch.float32, "lse", (batch.total_q, N_HEADS))
+    _need(ws, torch.uint8, "ws")
+
+
+def s5_dense_gqa_attn(k_pool, v_pool, batch: Batch, q, sm_scale: float, out, lse, ws, stream=None):
+    """Attention of the batch's new tokens over the whole cache (positions 0 .. t
+    of each row); ``lse`` may be None.  ``ws``: ``new_workspace(batch, dense=True)``."""
+    kv = _kv(k_pool, v_pool)
+    _dense_args(batch, q, out, lse, ws)
+    _check(_lib.s5_dense_gqa_attn(ctypes.byref(kv), ctypes.byref(batch.desc), _ptr(q), float(sm_scale), _ptr(out),
+                                  _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "s5_dense_gqa_attn")
+
+
+def s5_dense_gqa_attn_fp8kv(k_pool, v_pool, batch: Batch, q, sm_scale: float, k_scale: float, v_scale: float,
+                            out, lse, ws, stream=None):
+    """s5_dense_gqa_attn over one-byte KV: k_pool / v_pool uint8 E4M3 codes
+    [num_pages][4][64][192], a code standing for its value times k_scale / v_scale."""
+    _need(k_pool, torch.uint8, "k_pool")
+    _need(v_pool, torch.uint8, "v_pool", tuple(k_pool.shape))
+    sh = k_pool.shape
+    kv = KvDesc(k_pool.data_ptr(), v_pool.data_ptr(), sh[0], sh[2], sh[1], sh[3])
+    _dense_args(batch, q, out, lse, ws)
+    _check(_lib.s5_dense_gqa_attn_fp8kv(ctypes.byref(kv), ctypes.byref(batch.desc), _ptr(q), float(sm_scale),
+                                        float(k_scale), float(v_scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
+                                        _stream(stream)), "s5_dense_gqa_attn_fp8kv")
+
+
+def s5_build_batch(req_pages, req_ids, new_lens, free_pages, batch: Batch, slots, positions, pages_used, ws,
+                   stream=None):
+    """Build the step's tables on the GPU: ``batch.page_table`` and ``batch.cu_q``
+    (written), ``slots`` / ``positions`` of the new tokens [total_q] and
+    ``pages_used`` [1] (each may be None), from the requests' pages ``req_pages``
+    [num_reqs][stride] (which receives the pages taken from ``free_pages``), the
+    request of each sequence ``req_ids`` [batch] (-1: empty), ``batch.ctx_lens``
+    and ``new_lens`` [batch].  ``batch.total_q`` is the sum of the new tokens."""
+    _need(req_pages, torch.int32, "req_pages")
+    if req_pages.dim() != 2:
+        raise ValueError("req_pages must be [num_reqs][stride]")
+    n = batch.ctx_lens.numel()
+    _need(req_ids, torch.int32, "req_ids", (n,))
+    _need(new_lens, torch.int32, "new_lens", (n,))
+    _need(free_pages, torch.int32, "free_pages", (free_pages.numel(),))
+    if slots is not None:
+        _need(slots, torch.int32, "slots", (batch.total_q,))
+    if positions is not None:
+        _need(positions, torch.int32, "positions", (batch.total_q,))
+    if pages_used is not None:
+        _need(pages_used, torch.int32, "pages_used", (1,))
+    _need(ws, torch.uint8, "ws")
+    reqs = RequestDesc(req_pages.data_ptr(), free_pages.data_ptr(), req_pages.shape[0], req_pages.shape[1],
+                       free_pages.numel())
+    _check(_lib.s5_build_batch(ctypes.byref(reqs), _ptr(req_ids), _ptr(new_lens), ctypes.byref(batch.desc),
+                               _ptr(slots), _ptr(positions), _ptr(pages_used), _ptr(ws), ws.numel(),
+                               _stream(stream)), "s5_build_batch")
 
 
 def s5_reset_device_error(ws: torch.Tensor, stream=None):

@@ -88,8 +88,9 @@ typedef enum {
 
 /* ABI version (major * 100 + minor): 1.01 added the cache append, the
  * per-KV-group entry points and the one-byte-key indexer; 1.02 the sparse
- * attention over one-byte KV and its cache append. */
-#define S5_ABI_VERSION 102
+ * attention over one-byte KV and its cache append; 1.03 dense attention over
+ * the whole cache (bf16 and one-byte KV) and batch tables built on the GPU. */
+#define S5_ABI_VERSION 103
 
 /* One attention layer's paged KV cache. */
 typedef struct {
@@ -311,6 +312,87 @@ s5_status s5_append_kv(const s5_kv_desc *kv, const s5_index_desc *index, const s
 s5_status s5_append_kv_fp8(const s5_kv_desc *kv, const s5_index_desc *index, const s5_batch_desc *batch,
                            const void *k_new, const void *v_new, const void *key_new, float k_scale, float v_scale,
                            void *workspace, size_t workspace_bytes, s5_stream_t stream);
+
+/* Dense GQA over the whole cache: attention of a batch's new tokens with no
+ * selection and no window, for full-attention layers, for layers or requests
+ * whose history is short, and as the answer a sparse layer is compared with.
+ * For row r at position t and head h (group g = h / 16):
+ *   out = sum_{j <= t} softmax_j(sm_scale * q[r][h] . K[j][g]) V[j][g]
+ *   lse = log sum_{j <= t} exp(sm_scale * q[r][h] . K[j][g])   (may be NULL)
+ * A sequence's cache is split over as many CTAs as balance the batch (from the
+ * device's lengths, so ragged batches balance too) and the parts are joined by
+ * their log-sum-exp.  K or V values at positions > t never reach row r, not
+ * even as infinities or NaN.  A V value at a position <= t that is not finite
+ * makes its dimension of the row's 16 heads not finite (NaN or an infinity); a
+ * score that is NaN or +inf makes its row and head not finite; a score of -inf
+ * has weight 0, and a row and head whose scores are all -inf gives zeros and
+ * lse = -inf.
+ *   rows behind the batch: total_q may exceed cu_q[batch] (a batch padded to a
+ *     fixed size); rows from cu_q[batch] on are left as they were.
+ *   device faults (S5_ERR_DEVICE_BOUNDS): a sequence with ctx_lens < 0, row
+ *     offsets that decrease or leave [0, total_q], or ctx_lens + new tokens
+ *     above max_len gives zeros and lse = -inf in its rows (info = its first
+ *     row); the tokens of a page id outside the pool take no part (info = a
+ *     row that would read it).  Other rows are unaffected.
+ *   limits: total_q * 64 <= 2^31 - 1, num_pages * 256 < 2^31
+ *     (S5_ERR_UNSUPPORTED otherwise).
+ * The workspace is the one of s5_workspace_size_dense (which also covers every
+ * call that s5_workspace_size covers); its contents besides the error record
+ * carry nothing from call to call. */
+s5_status s5_workspace_size_dense(const s5_batch_desc *batch, int32_t window, size_t *bytes);
+s5_status s5_dense_gqa_attn(const s5_kv_desc *kv, const s5_batch_desc *batch, const void *q, float sm_scale, void *out,
+                            float *lse, void *workspace, size_t workspace_bytes, s5_stream_t stream);
+
+/* s5_dense_gqa_attn over one-byte KV: pools, codes and scales as in
+ * s5_sparse_gqa_attn_fp8kv.  k_scale, v_scale and sm_scale * k_scale must be
+ * finite (S5_ERR_INVALID_ARG). */
+s5_status s5_dense_gqa_attn_fp8kv(const s5_kv_desc *kv, const s5_batch_desc *batch, const void *q, float sm_scale,
+                                  float k_scale, float v_scale, void *out, float *lse, void *workspace,
+                                  size_t workspace_bytes, s5_stream_t stream);
+
+/* The requests a server holds and the pages it may hand out this step. */
+typedef struct {
+  int32_t *req_pages;        /* device int32 [num_reqs][req_stride]: the pages of request i, in order; WRITTEN  */
+  const int32_t *free_pages; /* device int32 [num_free]: page ids, taken from the front (may be NULL: none)     */
+  int32_t num_reqs;          /* >= 1 */
+  int32_t req_stride;        /* row stride of req_pages, >= 1 */
+  int32_t num_free;          /* >= 0 */
+} s5_request_desc;
+
+/* A step's batch tables, built on the GPU from the requests' lengths, before
+ * the step's appends and attention.  Sequence s is request id = req_ids[s]
+ * with ctx = ctx_lens[s] cached and new = new_lens[s] new tokens; it holds
+ * ceil(ctx / 64) pages, needs ceil((ctx + new) / 64), and takes the difference
+ * from free_pages, sequence by sequence and page by page:
+ *   page_table[s][p]  req_pages[id][p] for the held pages, the taken pages
+ *                     behind them, -1 up to max_pages
+ *   req_pages[id]     receives the taken pages in their places
+ *   cu_q[s]           sum of new over the sequences before s; cu_q[batch]: all
+ *   slots[r]          64 * page + offset of new token r in the pools' token
+ *                     order [page][offset] (-1: its page is missing)
+ *   positions[r]      its position t in the sequence
+ *   pages_used[0]     pages taken (the caller advances its list by as many)
+ * req_ids[s] = -1 is an empty sequence (a batch padded to a fixed size): its
+ * lengths are not read, its table row is -1.
+ *   batch        ctx_lens, batch, max_pages and total_q are read; page_table
+ *                and cu_q are WRITTEN (the descriptor's const applies to the
+ *                calls that read them).  max_q and max_len are not used.
+ *   slots, positions  device int32 [total_q], or NULL; entries from cu_q[batch]
+ *                on are left as they were
+ *   pages_used   device int32 [1], or NULL
+ *   workspace    at least S5_WS_FIXED_BYTES; only its error record is used
+ * Device faults (S5_ERR_DEVICE_BOUNDS, info = the sequence): a request id
+ * outside [-1, num_reqs), a negative length, ctx + new above S5_MAX_LEN or more
+ * pages than max_pages or req_stride make that sequence an empty one; a page
+ * that free_pages no longer has becomes -1, and so do the slots in it; new
+ * tokens beyond total_q are cut off (cu_q never exceeds total_q).
+ * A request may be in a batch once; page_table and req_pages must not overlap
+ * (S5_ERR_INVALID_ARG).  slots of a page id above 2^25 - 2 (64 * page past 32
+ * bits) are -1.
+ * Limits: at most 65,535 sequences, max_pages <= 2^20 (S5_ERR_UNSUPPORTED). */
+s5_status s5_build_batch(const s5_request_desc *requests, const int32_t *req_ids, const int32_t *new_lens,
+                         const s5_batch_desc *batch, int32_t *slots, int32_t *positions, int32_t *pages_used,
+                         void *workspace, size_t workspace_bytes, s5_stream_t stream);
 
 /* Zero the first S5_WS_FIXED_BYTES of a workspace: the device error record
  * and the partition counters (asynchronous, on `stream`). */
