@@ -480,18 +480,40 @@ s5_status workspace_need(const s5_batch_desc *batch, int32_t window, int groups,
 
 struct DenseWs {
   size_t part_o, part_ml, end;
-  int n_split;
+  int tile_rows, n_ctas;
 };
 
-DenseWs dense_ws(const s5_batch_desc *b) {
+// One persistent CTA per SM, fewer when the batch cannot have that many page
+// units (pages times KV groups, per tile of rows).
+DenseWs dense_ws(const s5_batch_desc *b, bool kv8, int sms) {
   DenseWs w{};
-  const long long units = (long long)b->total_q * kKv;
-  w.n_split = units > 0 ? (int)(592 / units) : 1;
-  w.n_split = w.n_split < 1 ? 1 : (w.n_split > 32 ? 32 : w.n_split);
+  const int cap = kv8 ? kDenseMaxRows8 : kDenseMaxRows;
+  w.tile_rows = 1;
+  while (w.tile_rows < cap && w.tile_rows < b->max_q) w.tile_rows *= 2;
+  const long long units = (long long)b->total_q * kKv * ((b->max_len + kPage - 1) / kPage);
+  w.n_ctas = (int)(units < sms ? (units < 1 ? 1 : units) : sms);
   w.part_o = kWsFixed;
-  w.part_ml = align_up(w.part_o + (size_t)b->total_q * kHeads * w.n_split * kD * sizeof(float), 256);
-  w.end = align_up(w.part_ml + (size_t)b->total_q * kHeads * w.n_split * 2 * sizeof(float), 256);
+  w.part_ml = align_up(w.part_o + (size_t)2 * w.n_ctas * w.tile_rows * kHpg * kD * sizeof(float), 256);
+  w.end = align_up(w.part_ml + (size_t)4 * w.n_ctas * 2 * w.tile_rows * kHpg * sizeof(float), 256);
   return w;
+}
+
+// A pool as rows of 192 dims in three planes of 64 (bf16: 128 bytes, one byte:
+// 64 bytes), one box the 64 tokens of a page's KV group: [plane][token][64
+// dims], swizzled over the plane's row width.
+bool make_page_map(CUtensorMap *m, const void *pool, int num_pages, bool kv8) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const int width = kv8 ? 1 : 2;
+  cuuint64_t dims[3] = {64, (cuuint64_t)num_pages * kKv * kPage, 3};
+  cuuint64_t strides[2] = {(cuuint64_t)kD * width, (cuuint64_t)64 * width};
+  cuuint32_t box[3] = {64, (cuuint32_t)kPage, 3};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, kv8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(pool),
+                  dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  kv8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
 }
 
 // kv8 as in attn_common.
@@ -506,12 +528,13 @@ s5_status dense_common(const s5_kv_desc *kv, const s5_batch_desc *b, const void 
   if (ws == nullptr) return S5_ERR_WORKSPACE;
   if (b->total_q == 0) return S5_OK;
   if (q == nullptr || out == nullptr || !aligned16(q) || !aligned16(out)) return S5_ERR_INVALID_ARG;
-  const DenseWs w = dense_ws(b);
+  const DenseWs w = dense_ws(b, kv8, device_slots() / kCtasPerSm);
   if (ws_bytes < w.end) return S5_ERR_WORKSPACE;
   uint8_t *wsb = static_cast<uint8_t *>(ws);
+  CUtensorMap tk, tv;
+  if (!make_page_map(&tk, kv->k_pool, kv->num_pages, kv8) || !make_page_map(&tv, kv->v_pool, kv->num_pages, kv8))
+    return S5_ERR_CUDA;
   DenseArgs a{};
-  a.k_pool = kv->k_pool;
-  a.v_pool = kv->v_pool;
   a.num_pages = kv->num_pages;
   a.q = q;
   a.page_table = b->page_table;
@@ -524,13 +547,16 @@ s5_status dense_common(const s5_kv_desc *kv, const s5_batch_desc *b, const void 
   a.scale_log2 = (kv8 ? sm_scale * k_scale : sm_scale) * 1.4426950408889634f;
   a.v_scale = kv8 ? v_scale : 1.f;
   a.kv8 = kv8 ? 1 : 0;
-  a.n_split = w.n_split;
+  a.tile_rows = w.tile_rows;
+  a.reread = b->max_q > w.tile_rows ? 1 : 0;
+  a.n_ctas = w.n_ctas;
   a.out = out;
   a.lse = lse;
   a.part_o = reinterpret_cast<float *>(wsb + w.part_o);
   a.part_ml = reinterpret_cast<float *>(wsb + w.part_ml);
+  a.cnt = reinterpret_cast<uint32_t *>(wsb + kWsHeader);
   a.err = reinterpret_cast<int32_t *>(ws);
-  return cuda_status(launch_dense(a, stream));
+  return cuda_status(launch_dense(a, tk, tv, stream));
 }
 
 // Block scores and top-k for `groups` indexer queries per token: q_index
@@ -703,8 +729,10 @@ s5_status s5_swa_gqa_attn(const s5_kv_desc *kv, const s5_batch_desc *batch, cons
 s5_status s5_workspace_size_dense(const s5_batch_desc *batch, int32_t window, size_t *bytes) {
   const s5_status st = workspace_need(batch, window, 1, bytes);
   if (st != S5_OK) return st;
-  const size_t dense = dense_ws(batch).end;
-  if (dense > *bytes) *bytes = dense;
+  for (const bool kv8 : {false, true}) {
+    const size_t dense = dense_ws(batch, kv8, kSizingSms).end;
+    if (dense > *bytes) *bytes = dense;
+  }
   return S5_OK;
 }
 

@@ -143,8 +143,10 @@ struct TileArgs {
 };
 
 // Dense attention over the whole cache.
+constexpr int kDenseMaxRows = 8;   // query rows per tile (8 rows x 16 heads = M 128), bf16 KV
+constexpr int kDenseMaxRows8 = 4;  // ... one-byte KV (the other half of M holds the weights' lower terms)
+
 struct DenseArgs {
-  const void *k_pool, *v_pool;
   int num_pages;
   const void *q;
   const int32_t *page_table;
@@ -157,14 +159,17 @@ struct DenseArgs {
   float scale_log2;  // sm_scale * log2(e) (one-byte KV: times k_scale)
   float v_scale;     // one-byte KV: value of a V code = v_scale * E4M3(code)
   int kv8;           // nonzero: K / V pools hold one-byte E4M3 codes
-  int n_split;
+  int tile_rows;     // query rows per tile: 1, 2, 4 or (bf16 KV) 8
+  int reread;        // nonzero: sequences may have several tiles, which read the same pages
+  int n_ctas;
   void *out;
   float *lse;
-  float *part_o;
-  float *part_ml;
+  float *part_o;   // [2 * n_ctas][tile_rows * 16][192]
+  float *part_ml;  // [4 * n_ctas][2][tile_rows * 16]: reference (log2) and sum of a part; joined parts behind
+  uint32_t *cnt;   // [3 * n_ctas] arrival counters, zero between calls
   int32_t *err;
 };
-cudaError_t launch_dense(const DenseArgs &a, cudaStream_t st);
+cudaError_t launch_dense(const DenseArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t st);
 
 // cudaFuncSetAttribute(kernel, MaxDynamicSharedMemorySize, bytes) on the
 // current device, skipped when an equal or larger value is already set there
