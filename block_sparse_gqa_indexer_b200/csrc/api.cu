@@ -498,18 +498,19 @@ DenseWs dense_ws(const s5_batch_desc *b, bool kv8, int sms) {
   return w;
 }
 
-// A pool as rows of 192 dims in three planes of 64 (bf16: 128 bytes, one byte:
-// 64 bytes), one box the 64 tokens of a page's KV group: [plane][token][64
-// dims], swizzled over the plane's row width.
+// A pool as 8-token groups of three planes of 64 dims (bf16: 128 bytes, one
+// byte: 64 bytes a token), one box the 8 groups of a page's KV group: [group]
+// [plane][8 tokens][64 dims], swizzled over the plane's row width.  The box
+// covers a page's 64 x 192 values, contiguous in memory.
 bool make_page_map(CUtensorMap *m, const void *pool, int num_pages, bool kv8) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const int width = kv8 ? 1 : 2;
-  cuuint64_t dims[3] = {64, (cuuint64_t)num_pages * kKv * kPage, 3};
-  cuuint64_t strides[2] = {(cuuint64_t)kD * width, (cuuint64_t)64 * width};
-  cuuint32_t box[3] = {64, (cuuint32_t)kPage, 3};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(m, kv8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(pool),
+  cuuint64_t dims[4] = {64, 8, 3, (cuuint64_t)num_pages * kKv * (kPage / 8)};
+  cuuint64_t strides[3] = {(cuuint64_t)kD * width, (cuuint64_t)64 * width, (cuuint64_t)8 * kD * width};
+  cuuint32_t box[4] = {64, 8, 3, (cuuint32_t)kPage / 8};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(m, kv8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pool),
                   dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   kv8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

@@ -20,16 +20,17 @@
 // arrive joins the group, the last group joins the groups (in CTA order, so
 // results do not depend on who is last).
 //
-// One CTA: warp 4 streams K and warp 5 V, a 64-token page of one KV group per
-// TMA copy, through rings of kStages pages; warp 6 issues S = Q K^T (M = 128,
-// N = 64 tokens) into two tensor-memory buffers, warp 7 O += P V (N = 192), both
-// with A (Q, P) in tensor memory; warps 0-3, one thread per MMA row, load Q, run
-// the softmax and finish each tile.
+// One CTA works in chunks of two pages (128 tokens): warp 4 streams K and warp
+// 5 V, one TMA copy per page and KV group, through rings of kStages chunks; warp
+// 6 issues S = Q K^T (M = N = 128) and warp 7 O += P V (N = 192), both with A (Q,
+// P) in tensor memory; warps 0-3, one thread per MMA row, load Q, run the softmax
+// and finish each tile.  (N = 64 products take 56 cycles instead of 32, so single
+// pages would cost the tensor pipe almost as much per page as chunks do per two.)
 //
 // The M = 128 rows for fewer than 128 (row, head) pairs.  MMA row
 //   m = ((c * kSlots + slot) * RT + j) * 16 + h
-// stands for tile row j, head h, copy c and slot.  A copy owns a run of 64 /
-// copies tokens of every page: its P is zero elsewhere, it has its own reference
+// stands for tile row j, head h, copy c and slot.  A copy owns a run of 128 /
+// copies tokens of every chunk: its P is zero elsewhere, it has its own reference
 // and sum, and the copies are joined at the end; so all 128 threads work on
 // the softmax of one decode row and none needs another's maximum.  A slot holds
 // one term of the weights, the last rounding's remainder scaled up, at no cost in
@@ -47,6 +48,7 @@ namespace {
 constexpr int kDnSoft = 128;  // softmax threads: warps 0-3
 constexpr int kDnThreads = 256;
 constexpr int kWarpK = 4, kWarpV = 5, kWarpS = 6, kWarpPv = 7;
+constexpr int kChunk = 2 * kPage;               // tokens
 constexpr int kScanPer = 4;                      // sequences per thread and round of the prefix sums
 constexpr int kScanSeqs = kDnThreads * kScanPer;
 constexpr uint64_t kDnWaitNs = 2000000000ull;    // 2 s per wait
@@ -55,8 +57,8 @@ constexpr int kMaxJoin = 16;                     // parts joined at a time (16 *
 constexpr float kLn2 = 0.69314718055994531f;
 
 // tensor memory columns
-constexpr uint32_t kTmS = 0;    // 2 x 64: S of page gc in buffer gc % 2
-constexpr uint32_t kTmP = 128;  // 2 x 32: P of page gc in buffer gc % 2
+constexpr uint32_t kTmS = 0;    // 128: S of a chunk
+constexpr uint32_t kTmP = 128;  // 64: P of a chunk (one byte: 32 per term)
 constexpr uint32_t kTmO = 192;  // 192: O
 constexpr uint32_t kTmQ = 384;  // 96: Q (bf16: two dims per column; one byte: two terms of 48 columns)
 constexpr uint32_t kTmCols = 512;
@@ -64,23 +66,27 @@ constexpr uint32_t kTmCols = 512;
 template <bool KV8, int RT>
 struct Cfg {
   // term slots.  bf16: the weight and its remainder, unless 8 rows take every MMA row.
-  // One byte: 4 one-term slots, or (4 rows) 2 slots of two terms each.
-  static constexpr int kSlots = KV8 ? (RT <= 2 ? 4 : 2) : (RT == 8 ? 1 : 2);
+  // One byte: 4 one-term slots, or (2 and 4 rows) 2 slots of two terms each.
+  static constexpr int kSlots = KV8 ? (RT == 1 ? 4 : 2) : (RT == 8 ? 1 : 2);
   static constexpr int kTerms = KV8 ? 4 / kSlots : 1;  // unscaled terms per slot (MMA passes of P V)
   static constexpr int kCopies = 8 / (RT * kSlots);
-  static constexpr int kTok = 64 / kCopies;            // tokens of a page per softmax thread
+  static constexpr int kTok = kChunk / kCopies;        // tokens of a chunk per softmax thread
   static constexpr int kPageBytes = kPage * kD * (KV8 ? 1 : 2);
-  static constexpr int kPlane = kPageBytes / 3;
-  static constexpr int kRowB = kPlane / kPage;         // bytes of a token in a plane
-  static constexpr int kStages = KV8 ? 8 : 4;          // pages per ring
+  // a page in shared memory: [8 groups of 8 tokens][3 planes of 64 dims][8 tokens][kRowB], so
+  // that 8-token groups are evenly spaced across the pages of a chunk
+  static constexpr int kRowB = KV8 ? 64 : 128;
+  static constexpr int kPlane = 8 * kRowB;
+  static constexpr int kGroup = 3 * kPlane;
+  static constexpr int kStages = KV8 ? 4 : 2;          // chunks per ring
+  static constexpr int kStageBytes = 2 * kPageBytes;
   // one byte: weights reach 2^8 and E4M3 terms 2^8 * 1.75, so the reference sits 6
   // binades above the maximum's: weights of 2^-20 of it keep 8 bits
   static constexpr float kOff = KV8 ? 6.f : 0.f;
   static constexpr float kSlotScale = KV8 ? (kTerms == 1 ? 16.f : 256.f) : 1.f;
   static_assert(kCopies >= 1 && kCopies * kSlots * RT == 8, "128 MMA rows");
   // shared memory (from a 1,024-byte aligned base)
-  static constexpr int kOffV = kStages * kPageBytes;
-  static constexpr int kOffStage = 2 * kStages * kPageBytes;  // float [2][128][20]: epilogue; join weights
+  static constexpr int kOffV = kStages * kStageBytes;
+  static constexpr int kOffStage = 2 * kStages * kStageBytes; // float [2][128][20]: epilogue; join weights
   static constexpr int kOffMl = kOffStage + 2 * 128 * 20 * 4; // float [2][128]: references and sums
   static constexpr int kOffBad = kOffMl + 2 * 128 * 4;        // uint32 [48]: per dim, rows that saw a non-finite value
   static constexpr int kOffBar = kOffBad + 192;
@@ -240,8 +246,10 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, float f) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// Q of one MMA row into tensor memory: bf16 as it is.
+// Q of one MMA row into tensor memory, negated when the scale is negative: bf16 as
+// it is.
 __device__ __forceinline__ void load_q_bf16(const DenseArgs &a, size_t qrow, bool on, uint32_t tq) {
+  const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
   const uint4 *src = reinterpret_cast<const uint4 *>(a.q) + qrow * (kD / 8);
 #pragma unroll
   for (int x = 0; x < kD / 32; ++x) {
@@ -249,10 +257,10 @@ __device__ __forceinline__ void load_q_bf16(const DenseArgs &a, size_t qrow, boo
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
       const uint4 v = on ? ld_cg(src + 4 * x + y) : make_uint4(0, 0, 0, 0);
-      w[4 * y] = v.x;
-      w[4 * y + 1] = v.y;
-      w[4 * y + 2] = v.z;
-      w[4 * y + 3] = v.w;
+      w[4 * y] = v.x ^ flip;
+      w[4 * y + 1] = v.y ^ flip;
+      w[4 * y + 2] = v.z ^ flip;
+      w[4 * y + 3] = v.w ^ flip;
     }
     tc::st_16cols(tq + 16 * x, w);
   }
@@ -280,7 +288,8 @@ __device__ __forceinline__ float load_q_e4m3(const DenseArgs &a, size_t qrow, bo
     }
   }
   const int e = (int)(__float_as_uint(top) >> 23);  // biased exponent of the largest magnitude
-  const float up = finite ? __uint_as_float((uint32_t)min(261 - e, 254) << 23) : __uint_as_float(0x7FC00000u);
+  float up = finite ? __uint_as_float((uint32_t)min(261 - e, 254) << 23) : __uint_as_float(0x7FC00000u);
+  if (a.scale_log2 < 0.f) up = -up;
   const float down = e > 7 ? __uint_as_float((uint32_t)(e - 7) << 23) : __uint_as_float(0x00400000u);
 #pragma unroll
   for (int x = 0; x < kD / 32; ++x) {
@@ -315,7 +324,7 @@ template <bool KV8, int RT>
 __global__ void __launch_bounds__(kDnThreads, 1)
     dense_kernel(const DenseArgs a, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<KV8, RT>;
-  constexpr int NS = C::kStages, PB = C::kPageBytes, kPairs = RT * kHpg;
+  constexpr int NS = C::kStages, PB = C::kPageBytes, SB = C::kStageBytes, kPairs = RT * kHpg;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sk = smem, *sv = smem + C::kOffV;
@@ -324,9 +333,9 @@ __global__ void __launch_bounds__(kDnThreads, 1)
   uint32_t *bad_s = reinterpret_cast<uint32_t *>(smem + C::kOffBad);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
   uint64_t *k_full = bars, *k_empty = bars + NS, *v_full = bars + 2 * NS, *v_empty = bars + 3 * NS;
-  uint64_t *s_full = bars + 4 * NS, *s_empty = s_full + 2, *p_full = s_full + 4, *p_free = s_full + 6;
-  uint64_t *q_full = s_full + 8, *q_empty = s_full + 9, *o_empty = s_full + 10, *b_soft = s_full + 11,
-           *b_flag = s_full + 12, *b_final = s_full + 13;
+  uint64_t *s_full = bars + 4 * NS, *s_empty = s_full + 1, *p_full = s_full + 2, *p_free = s_full + 3;
+  uint64_t *q_full = s_full + 4, *q_empty = s_full + 5, *o_empty = s_full + 6, *b_soft = s_full + 7,
+           *b_flag = s_full + 8, *b_final = s_full + 9;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
   int *abort_flag = reinterpret_cast<int *>(smem + C::kOffMisc + 4);
   int *flag_s = reinterpret_cast<int *>(smem + C::kOffMisc + 8);
@@ -340,12 +349,10 @@ __global__ void __launch_bounds__(kDnThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < 4 * NS; ++i) mbar_init(bars + i, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full + i, 1);
-      mbar_init(s_empty + i, 4);
-      mbar_init(p_full + i, 4);
-      mbar_init(p_free + i, 1);
-    }
+    mbar_init(s_full, 1);
+    mbar_init(s_empty, 4);
+    mbar_init(p_full, 4);
+    mbar_init(p_free, 1);
     mbar_init(q_full, 4);
     mbar_init(q_empty, 1);
     mbar_init(o_empty, 4);
@@ -463,17 +470,24 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       for (int c = 0; c < x.np && ok; c += 32) {
         const int nxt = c + 32 + lane < x.np ? ld_cg(pt + c + 32 + lane) : -1;
         const int m = min(32, x.np - c);
-        for (int i = 0; i < m; ++i, ++gc) {
-          const int page = __shfl_sync(0xffffffffu, ids, i);
+        for (int i = 0; i < m; i += 2, ++gc) {
+          const int page[2] = {__shfl_sync(0xffffffffu, ids, i), __shfl_sync(0xffffffffu, ids, i + 1)};
           int go = 1;
           if (lane == 0) {
             const int st = gc % NS;
             if (gc >= NS) go = wait(empty + st, ((gc / NS) - 1) & 1) ? 1 : 0;
             if (go) {
-              const bool page_ok = page >= 0 && page < a.num_pages;
-              mbar_arrive_expect_tx(full + st, page_ok ? (uint32_t)PB : 0u);
-              if (page_ok) tma_load_3d(ring + st * PB, map, 0, (page * kKv + x.g) * kPage, 0, full + st, policy);
-              else if (is_k) record_error(a.err, S5_ERR_DEVICE_BOUNDS, x.row0);
+              bool page_ok[2];
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                page_ok[y] = page[y] >= 0 && page[y] < a.num_pages;
+                if (!page_ok[y] && is_k && i + y < m) record_error(a.err, S5_ERR_DEVICE_BOUNDS, x.row0);
+              }
+              mbar_arrive_expect_tx(full + st, (page_ok[0] ? PB : 0) + (page_ok[1] ? PB : 0));
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                if (page_ok[y])
+                  tma_load_4d(ring + st * SB + y * PB, map, 0, 0, 0, (page[y] * kKv + x.g) * (kPage / 8), full + st, policy);
             }
           }
           if (!__shfl_sync(0xffffffffu, go, 0)) {
@@ -495,32 +509,35 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       bool ok = true;
       while (ok && walk.next(x)) {
         if (!wait(q_full, qi & 1)) break;
-        for (int c = 0; c < x.np; ++c, ++gc) {
-          const int st = gc % NS, sb = gc & 1;
-          if (!wait(k_full + st, (gc / NS) & 1) || (gc >= 2 && !wait(s_empty + sb, ((gc >> 1) - 1) & 1))) {
+        for (int c = 0; c < x.np; c += 2, ++gc) {
+          const int st = gc % NS;
+          if (!wait(k_full + st, (gc / NS) & 1) || (gc >= 1 && !wait(s_empty, (gc - 1) & 1))) {
             ok = false;
             break;
           }
           tc::fence_after_sync();
-          const uint32_t kb = k_base + st * PB, d = tmem + kTmS + sb * 64;
+          const uint32_t kb = k_base + st * SB;
+          const int n = c + 1 < x.np ? 2 * kPage : kPage;  // (a run's last page may stand alone)
           if constexpr (KV8) {
-            constexpr uint32_t idesc = tc::idesc_e4m3_f32(128, kPage, false);
+            const uint32_t idesc = tc::idesc_e4m3_f32(128, n, false);
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int kk = 0; kk < kD / 32; ++kk)
-                tc::mma_e4m3_ts(d, tmem + kTmQ + t * 48 + kk * 8,
-                                tc::smem_desc_sw64(kb + (kk >> 1) * C::kPlane + (kk & 1) * 32, 16, 512), idesc, t + kk > 0);
+                tc::mma_e4m3_ts(tmem + kTmS, tmem + kTmQ + t * 48 + kk * 8,
+                                tc::smem_desc_sw64(kb + (kk >> 1) * C::kPlane + (kk & 1) * 32, 16, C::kGroup), idesc,
+                                t + kk > 0);
           } else {
-            constexpr uint32_t idesc = tc::idesc_bf16_f32(128, kPage);
+            const uint32_t idesc = tc::idesc_bf16_f32(128, n);
 #pragma unroll
             for (int kk = 0; kk < kD / 16; ++kk)
-              tc::mma_bf16_ts(d, tmem + kTmQ + kk * 8, tc::smem_desc_k_sw128(kb + (kk >> 2) * C::kPlane + (kk & 3) * 32),
-                              idesc, kk > 0);
+              tc::mma_bf16_ts(tmem + kTmS, tmem + kTmQ + kk * 8,
+                              tc::smem_desc_k_sw128_stride(kb + (kk >> 2) * C::kPlane + (kk & 3) * 32, C::kGroup), idesc,
+                              kk > 0);
           }
           tc::commit(k_empty + st);
-          tc::commit(s_full + sb);
-          if (c == x.np - 1) tc::commit(q_empty);
+          tc::commit(s_full);
+          if (c + 2 >= x.np) tc::commit(q_empty);
         }
         ++qi;
       }
@@ -533,32 +550,35 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       int gc = 0, qi = 0;
       bool ok = true;
       while (ok && walk.next(x)) {
-        for (int c = 0; c < x.np; ++c, ++gc) {
-          const int st = gc % NS, pb = gc & 1;
-          if (!wait(p_full + pb, (gc >> 1) & 1) || !wait(v_full + st, (gc / NS) & 1) ||
+        for (int c = 0; c < x.np; c += 2, ++gc) {
+          const int st = gc % NS;
+          if (!wait(p_full, gc & 1) || !wait(v_full + st, (gc / NS) & 1) ||
               (c == 0 && qi > 0 && !wait(o_empty, (qi - 1) & 1))) {
             ok = false;
             break;
           }
           tc::fence_after_sync();
-          const uint32_t vb = v_base + st * PB, pa = tmem + kTmP + pb * 32;
+          const uint32_t vb = v_base + st * SB, pa = tmem + kTmP;
+          const int m = c + 1 < x.np ? 2 : 1;
           if constexpr (KV8) {
             constexpr uint32_t idesc = tc::idesc_e4m3_f32(128, kD, true);
 #pragma unroll
             for (int t = 0; t < C::kTerms; ++t)
 #pragma unroll
-              for (int ks = 0; ks < kPage / 32; ++ks)
-                tc::mma_e4m3_ts(tmem + kTmO, pa + t * 16 + ks * 8, tc::smem_desc_sw64(vb + ks * 2048, C::kPlane, 512), idesc,
-                                c + t + ks > 0);
+              for (int ks = 0; ks < 4; ++ks)
+                if (ks < 2 * m)
+                  tc::mma_e4m3_ts(tmem + kTmO, pa + t * 32 + ks * 8,
+                                  tc::smem_desc_sw64(vb + ks * 4 * C::kGroup, C::kPlane, C::kGroup), idesc, c + t + ks > 0);
           } else {
             constexpr uint32_t idesc = tc::idesc_bf16_f32_bmn(128, kD);
 #pragma unroll
-            for (int ks = 0; ks < kPage / 16; ++ks)
-              tc::mma_bf16_ts(tmem + kTmO, pa + ks * 8, tc::smem_desc_mn_sw128(vb + ks * 2048, C::kPlane, 1024), idesc,
-                              c + ks > 0);
+            for (int ks = 0; ks < 8; ++ks)
+              if (ks < 4 * m)
+                tc::mma_bf16_ts(tmem + kTmO, pa + ks * 8,
+                                tc::smem_desc_mn_sw128(vb + ks * 2 * C::kGroup, C::kPlane, C::kGroup), idesc, c + ks > 0);
           }
           tc::commit(v_empty + st);
-          tc::commit(p_free + pb);
+          tc::commit(p_free);
         }
         ++qi;
       }
@@ -589,7 +609,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
     while (ok && walk.next(x)) {
       const bool row_ok = j < x.nr;
       const int t_row = x.t0 + j, t_last = x.t0 + x.nr - 1;
-      float m_ref = -INFINITY, l = 0.f, sl2 = a.scale_log2;
+      float m_ref = -INFINITY, l = 0.f, sl2 = fabsf(a.scale_log2);
       if (qi > 0 && !wait_warp(q_empty, (qi - 1) & 1)) break;
       {
         const size_t qrow = (size_t)(x.row0 + j) * kHeads + x.g * kHpg + h;
@@ -602,61 +622,55 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       }
       const int32_t *pt = a.page_table + (size_t)x.s * a.max_pages + x.p0;
       int ids = -1, nxt = lane < x.np ? ld_cg(pt + lane) : -1;
-      for (int c = 0; c < x.np; ++c, ++gc) {
+      for (int c = 0; c < x.np; c += 2, ++gc) {
         if ((c & 31) == 0) {
           ids = nxt;
           nxt = c + 32 + lane < x.np ? ld_cg(pt + c + 32 + lane) : -1;
         }
-        const int page = __shfl_sync(0xffffffffu, ids, c & 31);
-        const bool page_ok = page >= 0 && page < a.num_pages;
+        // (a page behind the run's last reads as -1: no token of it is visible)
+        const int pa = __shfl_sync(0xffffffffu, ids, c & 31), pb = __shfl_sync(0xffffffffu, ids, (c & 31) + 1);
+        const bool ok_a = pa >= 0 && pa < a.num_pages, ok_b = pb >= 0 && pb < a.num_pages;
         const int base = (x.p0 + c) * kPage;
-        // tokens 0 .. lim of this thread's run are visible to its row
-        const bool masked = !page_ok || base + kPage - 1 > x.t0;
-        const int lim = page_ok ? t_row - base - cp * TOK : -1;
-        const int sb = gc & 1;
-        const float mu = (m_ref == -INFINITY) ? 0.f : m_ref;
-        if (!wait_warp(s_full + sb, (gc >> 1) & 1)) {
+        const bool masked = !ok_a || !ok_b || base + kChunk - 1 > x.t0;
+        // tokens 0 .. lim of this thread's run are visible to its row, past the 64th those to lim_b
+        const int lim0 = t_row - base - cp * TOK;
+        const int lim = (TOK == kChunk || cp * TOK < kPage ? ok_a : ok_b) ? lim0 : -1;
+        const int lim_b = ok_b ? lim0 : -1;
+        if (!wait_warp(s_full, gc & 1)) {
           ok = false;
           break;
         }
         tc::fence_after_sync();
         uint32_t v[TOK];
-        {
-          const uint32_t ts = tl + kTmS + sb * 64 + cp * TOK;
-          if constexpr (TOK == 16) tc::ld_16cols(ts, *reinterpret_cast<uint32_t(*)[16]>(v));
-          else
 #pragma unroll
-            for (int i = 0; i < TOK / 32; ++i) tc::ld_32cols(ts + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * i));
-        }
+        for (int i = 0; i < TOK / 32; ++i)
+          tc::ld_32cols(tl + kTmS + cp * TOK + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * i));
         tc::wait_ld();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s_empty + sb);
-        // scores relative to the reference, in log2 units
-        float sc[TOK];
+        if (lane == 0) mbar_arrive(s_empty);
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < TOK; ++i)
+            if (i > (i < kPage ? lim : lim_b)) v[i] = 0xFF800000u;  // -inf
+        }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < TOK; i += 2) {
-          float2 s2 = fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), make_float2(sl2, sl2),
-                           make_float2(-mu, -mu));
-          if (masked) {
-            if (i > lim) s2.x = -INFINITY;
-            if (i + 1 > lim) s2.y = -INFINITY;
-          }
-          sc[i] = s2.x;
-          sc[i + 1] = s2.y;
-          mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], s2.x, s2.y);
-        }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        for (int i = 0; i < TOK; i += 2)
+          mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+        // scores in log2 units are sl2 * S (sl2 >= 0: a negative scale's sign is in Q)
+        const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float top = raw == -INFINITY ? raw : raw * sl2;
         // the reference moves only when a weight would exceed 2^8 (or with the first finite score)
-        const bool grow = (m_ref == -INFINITY) ? (top > -INFINITY) : (top > 8.f);
-        const float shift = grow ? top - C::kOff : 0.f;
-        const bool resc = grow && m_ref != -INFINITY;
-        if (grow) m_ref = mu + shift;
+        const bool first = m_ref == -INFINITY;
+        const bool grow = first ? top > -INFINITY : top - m_ref > 8.f;
+        const bool resc = grow && !first;
+        const float m_old = m_ref;
+        if (grow) m_ref = top - C::kOff;
         if (__any_sync(0xffffffffu, resc)) {
-          const float corr = resc ? hw_exp2(-shift) : 1.f;
-          if (c > 0) {  // O holds the pages before: after their last product
-            if (!wait_warp(p_free + ((gc - 1) & 1), ((gc - 1) >> 1) & 1)) {
+          const float corr = resc ? hw_exp2(m_old - m_ref) : 1.f;
+          if (c > 0) {  // O holds the chunks before: after their last product
+            if (!wait_warp(p_free, (gc - 1) & 1)) {
               ok = false;
               break;
             }
@@ -674,16 +688,10 @@ __global__ void __launch_bounds__(kDnThreads, 1)
           }
           l *= corr;
         }
-        if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-          for (int i = 0; i < TOK; i += 2) {
-            const float2 d2 = add2(make_float2(sc[i], sc[i + 1]), make_float2(-shift, -shift));
-            sc[i] = d2.x;
-            sc[i + 1] = d2.y;
-          }
-        }
+        const float mu = (m_ref == -INFINITY) ? 0.f : m_ref;
         float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // this slot's term of the weights
+        // this slot's term of the weights, in place of the scores: term t of token i in byte or half
+        // i of pk[t]
         uint32_t pk[C::kTerms][TOK / (KV8 ? 4 : 2)];
         if constexpr (KV8) {
 #pragma unroll
@@ -693,7 +701,13 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < TOK; i += 2) {
-          const float2 p2 = make_float2(hw_exp2(sc[i]), hw_exp2(sc[i + 1]));
+          const float2 s2 = fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), make_float2(sl2, sl2),
+                                 make_float2(-mu, -mu));
+          float2 p2 = make_float2(hw_exp2(s2.x), hw_exp2(s2.y));
+          if (masked) {  // (a scale of 0 makes -inf NaN)
+            if (i > (i < kPage ? lim : lim_b)) p2.x = 0.f;
+            if (i + 1 > (i < kPage ? lim : lim_b)) p2.y = 0.f;
+          }
           ps[(i >> 1) & 1] = add2(ps[(i >> 1) & 1], p2);
           if constexpr (KV8) {
             // the weight in f16 (11 bits), then E4M3 terms of what is left
@@ -722,15 +736,16 @@ __global__ void __launch_bounds__(kDnThreads, 1)
           }
         }
         l += (ps[0].x + ps[1].x) + (ps[0].y + ps[1].y);
-        // P into buffer sb, last read by the product of page gc - 2
-        if (gc >= 2 && !wait_warp(p_free + sb, ((gc >> 1) - 1) & 1)) {
+        // P, last read by the product of the chunk before
+        if (gc >= 1 && !wait_warp(p_free, (gc - 1) & 1)) {
           ok = false;
           break;
         }
+        tc::fence_after_sync();
         constexpr int PC = TOK / (KV8 ? 4 : 2);  // columns of a term
 #pragma unroll
         for (int t = 0; t < C::kTerms; ++t) {
-          const uint32_t tp = tl + kTmP + sb * 32 + t * 16 + cp * PC;
+          const uint32_t tp = tl + kTmP + t * 32 + cp * PC;
           if constexpr (PC == 8) tc::st_8cols(tp, *reinterpret_cast<const uint32_t(*)[8]>(pk[t]));
           else
 #pragma unroll
@@ -745,19 +760,22 @@ __global__ void __launch_bounds__(kDnThreads, 1)
             ok = false;
             break;
           }
-          uint8_t *vb = sv + st * PB;
+          uint8_t *vb = sv + st * SB;
           constexpr int kPieces = C::kRowB / 16;  // 16-byte pieces of a token in a plane
-          const int first = page_ok ? max(x.t0 + 1 - base, 0) : 0;
-          for (int i = first * 3 * kPieces + tid; i < kPage * 3 * kPieces; i += kDnSoft) {
+          const int n_tok = c + 1 < x.np ? kChunk : kPage;
+          // from the first token of a bad page, or the first that some row does not see
+          const int first_tok = !ok_a ? 0 : min(max(x.t0 + 1 - base, 0), ok_b ? kChunk : kPage);
+          for (int i = first_tok * 3 * kPieces + tid; i < n_tok * 3 * kPieces; i += kDnSoft) {
             const int tok = i / (3 * kPieces), y = i % (3 * kPieces), plane = y / kPieces, piece = y % kPieces;
-            uint4 *at = reinterpret_cast<uint4 *>(vb + plane * C::kPlane + tok * C::kRowB + piece * 16);
-            if (!page_ok || base + tok > t_last) {
+            uint4 *at = reinterpret_cast<uint4 *>(vb + (tok >> 3) * C::kGroup + plane * C::kPlane + (tok & 7) * C::kRowB +
+                                                  piece * 16);
+            if (!(tok < kPage ? ok_a : ok_b) || base + tok > t_last) {
               *at = make_uint4(0, 0, 0, 0);
-            } else {
+            } else if (base + tok > x.t0) {
               const int swz = KV8 ? (tok >> 1) & 3 : tok & 7;
               const int d0 = plane * 64 + (piece ^ swz) * (KV8 ? 16 : 8);
               // rows whose position is at least the token's
-              const uint32_t rows = (0xFFu << max(base + tok - x.t0, 0)) & 0xFFu;
+              const uint32_t rows = (0xFFu << (base + tok - x.t0)) & 0xFFu;
               uint32_t w[4] = {at->x, at->y, at->z, at->w};
               bool hit = false;
 #pragma unroll
@@ -779,7 +797,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + sb);
+        if (lane == 0) mbar_arrive(p_full);
       }
       if (!ok) break;
 
@@ -820,7 +838,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
           ml[kPairs + pr] = L;
         }
       }
-      if (!wait_warp(p_free + ((gc - 1) & 1), ((gc - 1) >> 1) & 1)) {
+      if (!wait_warp(p_free, (gc - 1) & 1)) {
         ok = false;
         break;
       }
