@@ -33,8 +33,12 @@
 // copies tokens of every chunk: its P is zero elsewhere, it has its own reference
 // and sum, and the copies are joined at the end; so all 128 threads work on
 // the softmax of one decode row and none needs another's maximum.  A slot holds
-// one term of the weights, the last rounding's remainder scaled up, at no cost in
-// MMAs: two terms carry a weight to 2^-15 in bf16 (8 rows: one term, 2^-8).
+// one term of the weights, the remainder of the terms before it, at no cost in
+// MMAs: two terms carry a weight to 2^-15 in bf16 (8 rows: one term, 2^-8).  One
+// byte: the weight in f16 (2^-12), whose upper byte is an E5M2 value; four such
+// bytes, each of what the ones before leave, hold an f16 above 2^-16 exactly.
+// (E4M3 terms took 7 conversions per pair of weights, at 8 cycles each: 2,000
+// cycles of a chunk, against 370 for these.)
 #include <cuda.h>
 
 #include "s5_common.cuh"
@@ -79,10 +83,11 @@ struct Cfg {
   static constexpr int kGroup = 3 * kPlane;
   static constexpr int kStages = KV8 ? 4 : 2;          // chunks per ring
   static constexpr int kStageBytes = 2 * kPageBytes;
-  // one byte: weights reach 2^8 and E4M3 terms 2^8 * 1.75, so the reference sits 6
-  // binades above the maximum's: weights of 2^-20 of it keep 8 bits
-  static constexpr float kOff = KV8 ? 6.f : 0.f;
-  static constexpr float kSlotScale = KV8 ? (kTerms == 1 ? 16.f : 256.f) : 1.f;
+  // The reference sits kOff binades under the maximum it was taken from and moves when a weight
+  // would exceed 2^kTop.  One byte: f16 weights reach 2^15, E5M2 ones go down to 2^-16, so
+  // weights of 2^-28 of the largest still count.
+  static constexpr float kOff = KV8 ? 12.f : 0.f;
+  static constexpr float kTop = KV8 ? 15.f : 8.f;
   static_assert(kCopies >= 1 && kCopies * kSlots * RT == 8, "128 MMA rows");
   // shared memory (from a 1,024-byte aligned base)
   static constexpr int kOffV = kStages * kStageBytes;
@@ -239,10 +244,6 @@ __device__ __forceinline__ uint32_t float2_to_f16x2(float lo, float hi) {
 }
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   const __half2 v = __hsub2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
-  return *reinterpret_cast<const uint32_t *>(&v);
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, float f) {
-  const __half2 v = __hmul2(*reinterpret_cast<__half2 *>(&a), __float2half2_rn(f));
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
@@ -519,12 +520,12 @@ __global__ void __launch_bounds__(kDnThreads, 1)
           const uint32_t kb = k_base + st * SB;
           const int n = c + 1 < x.np ? 2 * kPage : kPage;  // (a run's last page may stand alone)
           if constexpr (KV8) {
-            const uint32_t idesc = tc::idesc_e4m3_f32(128, n, false);
+            const uint32_t idesc = tc::idesc_f8_f32(128, n, 0, false);
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int kk = 0; kk < kD / 32; ++kk)
-                tc::mma_e4m3_ts(tmem + kTmS, tmem + kTmQ + t * 48 + kk * 8,
+                tc::mma_f8_ts(tmem + kTmS, tmem + kTmQ + t * 48 + kk * 8,
                                 tc::smem_desc_sw64(kb + (kk >> 1) * C::kPlane + (kk & 1) * 32, 16, C::kGroup), idesc,
                                 t + kk > 0);
           } else {
@@ -561,13 +562,13 @@ __global__ void __launch_bounds__(kDnThreads, 1)
           const uint32_t vb = v_base + st * SB, pa = tmem + kTmP;
           const int m = c + 1 < x.np ? 2 : 1;
           if constexpr (KV8) {
-            constexpr uint32_t idesc = tc::idesc_e4m3_f32(128, kD, true);
+            constexpr uint32_t idesc = tc::idesc_f8_f32(128, kD, 1, true);
 #pragma unroll
             for (int t = 0; t < C::kTerms; ++t)
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
                 if (ks < 2 * m)
-                  tc::mma_e4m3_ts(tmem + kTmO, pa + t * 32 + ks * 8,
+                  tc::mma_f8_ts(tmem + kTmO, pa + t * 32 + ks * 8,
                                   tc::smem_desc_sw64(vb + ks * 4 * C::kGroup, C::kPlane, C::kGroup), idesc, c + t + ks > 0);
           } else {
             constexpr uint32_t idesc = tc::idesc_bf16_f32_bmn(128, kD);
@@ -610,11 +611,13 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       const bool row_ok = j < x.nr;
       const int t_row = x.t0 + j, t_last = x.t0 + x.nr - 1;
       float m_ref = -INFINITY, l = 0.f, sl2 = fabsf(a.scale_log2);
+      // (a score of -inf, masked or not, has weight 0 with a scale of 0 too)
       if (qi > 0 && !wait_warp(q_empty, (qi - 1) & 1)) break;
       {
         const size_t qrow = (size_t)(x.row0 + j) * kHeads + x.g * kHpg + h;
         if constexpr (KV8) sl2 *= load_q_e4m3(a, qrow, row_ok, tl + kTmQ);
         else load_q_bf16(a, qrow, row_ok, tl + kTmQ);
+        sl2 = fmaxf(sl2, 1e-37f);
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
@@ -660,10 +663,10 @@ __global__ void __launch_bounds__(kDnThreads, 1)
           mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
         // scores in log2 units are sl2 * S (sl2 >= 0: a negative scale's sign is in Q)
         const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const float top = raw == -INFINITY ? raw : raw * sl2;
-        // the reference moves only when a weight would exceed 2^8 (or with the first finite score)
+        const float top = raw * sl2;
+        // the reference moves only when a weight would exceed 2^kTop (or with the first finite score)
         const bool first = m_ref == -INFINITY;
-        const bool grow = first ? top > -INFINITY : top - m_ref > 8.f;
+        const bool grow = first ? top > -INFINITY : top - m_ref > C::kTop;
         const bool resc = grow && !first;
         const float m_old = m_ref;
         if (grow) m_ref = top - C::kOff;
@@ -690,49 +693,40 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         }
         const float mu = (m_ref == -INFINITY) ? 0.f : m_ref;
         float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // this slot's term of the weights, in place of the scores: term t of token i in byte or half
-        // i of pk[t]
+        // this slot's term of the weights: the upper half (one byte: E5M2 byte) of what the slots
+        // before it, taking the same toward zero, leave
         uint32_t pk[C::kTerms][TOK / (KV8 ? 4 : 2)];
-        if constexpr (KV8) {
 #pragma unroll
-          for (int t = 0; t < C::kTerms; ++t)
+        for (int i = 0; i < TOK; i += KV8 ? 4 : 2) {
+          float2 p2[2];
 #pragma unroll
-            for (int i = 0; i < TOK / 4; ++i) pk[t][i] = 0;
-        }
-#pragma unroll
-        for (int i = 0; i < TOK; i += 2) {
-          const float2 s2 = fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), make_float2(sl2, sl2),
-                                 make_float2(-mu, -mu));
-          float2 p2 = make_float2(hw_exp2(s2.x), hw_exp2(s2.y));
-          if (masked) {  // (a scale of 0 makes -inf NaN)
-            if (i > (i < kPage ? lim : lim_b)) p2.x = 0.f;
-            if (i + 1 > (i < kPage ? lim : lim_b)) p2.y = 0.f;
+          for (int y = 0; y < (KV8 ? 2 : 1); ++y) {
+            const float2 s2 = fma2(make_float2(__uint_as_float(v[i + 2 * y]), __uint_as_float(v[i + 2 * y + 1])),
+                                   make_float2(sl2, sl2), make_float2(-mu, -mu));
+            p2[y] = make_float2(hw_exp2(s2.x), hw_exp2(s2.y));
+            ps[y ^ ((i >> 1) & 1)] = add2(ps[y ^ ((i >> 1) & 1)], p2[y]);
           }
-          ps[(i >> 1) & 1] = add2(ps[(i >> 1) & 1], p2);
           if constexpr (KV8) {
-            // the weight in f16 (11 bits), then E4M3 terms of what is left
-            uint32_t r = float2_to_f16x2(p2.x, p2.y);
+            uint32_t r[2] = {float2_to_f16x2(p2[0].x, p2[0].y), float2_to_f16x2(p2[1].x, p2[1].y)};
 #pragma unroll
-            for (int y = 0; y < C::kSlots - 1; ++y) {
-              uint32_t w = r;
+            for (int y = 0; y < (C::kSlots - 1) * C::kTerms; ++y)
 #pragma unroll
-              for (int t = 0; t < C::kTerms; ++t) w = sub_f16x2(w, e4m3x2_to_f16x2(f16x2_to_e4m3x2(w)));
-              w = mul_f16x2(w, C::kSlotScale);
-              r = slot > y ? w : r;
-            }
+              for (int z = 0; z < 2; ++z) r[z] = sub_f16x2(r[z], r[z] & (slot * C::kTerms > y ? 0xFF00FF00u : 0u));
 #pragma unroll
             for (int t = 0; t < C::kTerms; ++t) {
-              const uint32_t code = f16x2_to_e4m3x2(r);
-              pk[t][i / 4] |= code << (8 * (i & 2));
-              if (t + 1 < C::kTerms) r = sub_f16x2(r, e4m3x2_to_f16x2(code));
+              pk[t][i / 4] = __byte_perm(r[0], r[1], 0x7531);
+              if (t + 1 < C::kTerms)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) r[z] = sub_f16x2(r[z], r[z] & 0xFF00FF00u);
             }
           } else if constexpr (C::kSlots == 2) {
-            // the upper 16 bits (toward zero), then the upper 16 bits of the exact remainder
-            const uint32_t b0 = __float_as_uint(p2.x), b1 = __float_as_uint(p2.y);
-            const float r0 = p2.x - __uint_as_float(b0 & 0xFFFF0000u), r1 = p2.y - __uint_as_float(b1 & 0xFFFF0000u);
-            pk[0][i / 2] = slot ? __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632) : __byte_perm(b0, b1, 0x7632);
+            const uint32_t cut = slot ? 0xFFFF0000u : 0u;
+            const float2 r = fma2(make_float2(__uint_as_float(__float_as_uint(p2[0].x) & cut),
+                                              __uint_as_float(__float_as_uint(p2[0].y) & cut)),
+                                  make_float2(-1.f, -1.f), p2[0]);
+            pk[0][i / 2] = __byte_perm(__float_as_uint(r.x), __float_as_uint(r.y), 0x7632);
           } else {
-            pk[0][i / 2] = pack_bf16(p2.x, p2.y);
+            pk[0][i / 2] = pack_bf16(p2[0].x, p2[0].y);
           }
         }
         l += (ps[0].x + ps[1].x) + (ps[0].y + ps[1].y);
@@ -816,12 +810,8 @@ __global__ void __launch_bounds__(kDnThreads, 1)
 #pragma unroll
       for (int i = 0; i < C::kCopies; ++i)
         L += hw_exp2(ml_s[i * kPairs * C::kSlots + pr] - Mu) * ml_s[128 + i * kPairs * C::kSlots + pr];
-      float down = 1.f;  // this slot's terms were scaled up
-#pragma unroll
-      for (int y = 1; y < C::kSlots; ++y)
-        if (slot >= y) down *= 1.f / C::kSlotScale;
       const bool whole = x.np == x.tile_pages;
-      const float own = hw_exp2(m_ref - Mu) * down * (whole ? (L == 0.f ? 0.f : a.v_scale / L) : 1.f);
+      const float own = hw_exp2(m_ref - Mu) * (whole ? (L == 0.f ? 0.f : a.v_scale / L) : 1.f);
       // parts of a tile: CTA index within the tile, its slot of partial results
       const int c_first = whole ? 0 : (int)(x.tile_u / chunk);
       const int n_parts = whole ? 1 : (int)((x.tile_u + x.tile_pages - 1) / chunk) - c_first + 1;

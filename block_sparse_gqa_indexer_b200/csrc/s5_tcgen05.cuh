@@ -98,10 +98,11 @@ __device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr, uint32_t lbo,
   return d;
 }
 
-// Instruction descriptor of kind::f8f6f4 with E4M3 A and B (format 0), fp32
-// accumulate; `b_mn`: B is MN-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool b_mn) {
-  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor of kind::f8f6f4, fp32 accumulate: `a_fmt` the format of
+// A (0: E4M3, 1: E5M2), B E4M3; `b_mn`: B is MN-major.
+__host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, int a_fmt, bool b_mn) {
+  return (1u << 4) | ((uint32_t)a_fmt << 7) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
 }
 
 // ---- MMA ----------------------------------------------------------------------
@@ -128,10 +129,10 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
-// One-byte operands (E4M3), A in tensor memory: M rows (lanes) x 32 elements (8
+// One-byte operands, A in tensor memory: M rows (lanes) x 32 elements (8
 // columns, four consecutive K elements per 32-bit column, the lowest K in the
 // low byte); one K=32 step.
-__device__ __forceinline__ void mma_e4m3_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+__device__ __forceinline__ void mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                             bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
