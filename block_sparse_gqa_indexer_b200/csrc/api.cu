@@ -485,11 +485,10 @@ struct DenseWs {
 
 // One persistent CTA per SM, fewer when the batch cannot have that many page
 // units (pages times KV groups, per tile of rows).
-DenseWs dense_ws(const s5_batch_desc *b, bool kv8, int sms) {
+DenseWs dense_ws(const s5_batch_desc *b, int sms) {
   DenseWs w{};
-  const int cap = kv8 ? kDenseMaxRows8 : kDenseMaxRows;
   w.tile_rows = 1;
-  while (w.tile_rows < cap && w.tile_rows < b->max_q) w.tile_rows *= 2;
+  while (w.tile_rows < kDenseMaxRows && w.tile_rows < b->max_q) w.tile_rows *= 2;
   const long long units = (long long)b->total_q * kKv * ((b->max_len + kPage - 1) / kPage);
   w.n_ctas = (int)(units < sms ? (units < 1 ? 1 : units) : sms);
   w.part_o = kWsFixed;
@@ -529,7 +528,7 @@ s5_status dense_common(const s5_kv_desc *kv, const s5_batch_desc *b, const void 
   if (ws == nullptr) return S5_ERR_WORKSPACE;
   if (b->total_q == 0) return S5_OK;
   if (q == nullptr || out == nullptr || !aligned16(q) || !aligned16(out)) return S5_ERR_INVALID_ARG;
-  const DenseWs w = dense_ws(b, kv8, device_slots() / kCtasPerSm);
+  const DenseWs w = dense_ws(b, device_slots() / kCtasPerSm);
   if (ws_bytes < w.end) return S5_ERR_WORKSPACE;
   uint8_t *wsb = static_cast<uint8_t *>(ws);
   CUtensorMap tk, tv;
@@ -730,10 +729,8 @@ s5_status s5_swa_gqa_attn(const s5_kv_desc *kv, const s5_batch_desc *batch, cons
 s5_status s5_workspace_size_dense(const s5_batch_desc *batch, int32_t window, size_t *bytes) {
   const s5_status st = workspace_need(batch, window, 1, bytes);
   if (st != S5_OK) return st;
-  for (const bool kv8 : {false, true}) {
-    const size_t dense = dense_ws(batch, kv8, kSizingSms).end;
-    if (dense > *bytes) *bytes = dense;
-  }
+  const size_t dense = dense_ws(batch, kSizingSms).end;
+  if (dense > *bytes) *bytes = dense;
   return S5_OK;
 }
 

@@ -21,24 +21,24 @@
 // results do not depend on who is last).
 //
 // One CTA works in chunks of two pages (128 tokens): warp 4 streams K and warp
-// 5 V, one TMA copy per page and KV group, through rings of kStages chunks; warp
-// 6 issues S = Q K^T (M = N = 128) and warp 7 O += P V (N = 192), both with A (Q,
-// P) in tensor memory; warps 0-3, one thread per MMA row, load Q, run the softmax
-// and finish each tile.  (N = 64 products take 56 cycles instead of 32, so single
-// pages would cost the tensor pipe almost as much per page as chunks do per two.)
+// 5 V, one TMA copy per page and KV group, through rings in shared memory; warp 6
+// issues S^T = K Q^T (M = 128 tokens, N = heads of the tile) into tensor memory;
+// warps 0-3, one thread per token, turn a row of S^T into weights P and store
+// them as the N operand of O^T += V^T P^T, which warp 7 issues (M = 128 + 64
+// dims); O^T stays in tensor memory until the tile's run of pages ends.
 //
-// The M = 128 rows for fewer than 128 (row, head) pairs.  MMA row
-//   m = ((c * kSlots + slot) * RT + j) * 16 + h
-// stands for tile row j, head h, copy c and slot.  A copy owns a run of 128 /
-// copies tokens of every chunk: its P is zero elsewhere, it has its own reference
-// and sum, and the copies are joined at the end; so all 128 threads work on
-// the softmax of one decode row and none needs another's maximum.  A slot holds
-// one term of the weights, the remainder of the terms before it, at no cost in
-// MMAs: two terms carry a weight to 2^-15 in bf16 (8 rows: one term, 2^-8).  One
-// byte: the weight in f16 (2^-12), whose upper byte is an E5M2 value; four such
-// bytes, each of what the ones before leave, hold an f16 above 2^-16 exactly.
-// (E4M3 terms took 7 conversions per pair of weights, at 8 cycles each: 2,000
-// cycles of a chunk, against 370 for these.)
+// Tokens and dims are the M side so that no product is wasted: a decode row has
+// only 16 heads per KV group, and with heads as M = 128 rows (copies of the heads
+// in the spare rows, each working on a run of tokens) the same stream ran at 2.18
+// ms for 32 x 131,072 bf16 tokens with the clock down to 1.06 GHz for the
+// power that the redundant products drew.  An MMA of N <= 32 takes 45 cycles, N =
+// 64 takes 50, N = 128 66, whatever the types.
+//
+// Weights are held in terms, each a column of P: bf16 KV the upper half of the
+// fp32 weight and the upper half of the remainder (2^-15); one-byte KV the weight
+// in f16, whose upper byte is an E5M2 value, as bytes of what the terms before
+// leave: four hold an f16 exactly above 2^-16 (weights to 2^-12), three with the
+// last rounded are within 2^-9.  Column sums need no split: fp32 in registers.
 #include <cuda.h>
 
 #include "s5_common.cuh"
@@ -52,53 +52,58 @@ namespace {
 constexpr int kDnSoft = 128;  // softmax threads: warps 0-3
 constexpr int kDnThreads = 256;
 constexpr int kWarpK = 4, kWarpV = 5, kWarpS = 6, kWarpPv = 7;
-constexpr int kChunk = 2 * kPage;               // tokens
+constexpr int kChunk = 2 * kPage;                // tokens
 constexpr int kScanPer = 4;                      // sequences per thread and round of the prefix sums
 constexpr int kScanSeqs = kDnThreads * kScanPer;
 constexpr uint64_t kDnWaitNs = 2000000000ull;    // 2 s per wait
-constexpr uint32_t kDnHintNs = 1000;
 constexpr int kMaxJoin = 16;                     // parts joined at a time (16 * 16 >= CTAs)
 constexpr float kLn2 = 0.69314718055994531f;
 
-// tensor memory columns
-constexpr uint32_t kTmS = 0;    // 128: S of a chunk
-constexpr uint32_t kTmP = 128;  // 64: P of a chunk (one byte: 32 per term)
-constexpr uint32_t kTmO = 192;  // 192: O
-constexpr uint32_t kTmQ = 384;  // 96: Q (bf16: two dims per column; one byte: two terms of 48 columns)
-constexpr uint32_t kTmCols = 512;
-
 template <bool KV8, int RT>
 struct Cfg {
-  // term slots.  bf16: the weight and its remainder, unless 8 rows take every MMA row.
-  // One byte: 4 one-term slots, or (2 and 4 rows) 2 slots of two terms each.
-  static constexpr int kSlots = KV8 ? (RT == 1 ? 4 : 2) : (RT == 8 ? 1 : 2);
-  static constexpr int kTerms = KV8 ? 4 / kSlots : 1;  // unscaled terms per slot (MMA passes of P V)
-  static constexpr int kCopies = 8 / (RT * kSlots);
-  static constexpr int kTok = kChunk / kCopies;        // tokens of a chunk per softmax thread
+  static constexpr int kPairs = RT * kHpg;            // (row, head) pairs of a tile: columns of S^T and O^T
+  static constexpr int kQTerms = KV8 ? 2 : 1;         // terms of q (rows of the N operand)
+  static constexpr int kS = kPairs * kQTerms;         // columns of S^T
+  static constexpr int kTerms = KV8 ? (RT == 4 ? 3 : 4) : 2;
+  static constexpr int kP = kPairs * kTerms;          // columns of P and O^T
+  static constexpr int kSBuf = 2 * kS + 2 * kP <= 512 ? 2 : 1;
+  // tensor memory: S^T buffers, O^T of dims 0-127, O^T of dims 128-191 (M = 64)
+  static constexpr uint32_t kTmO = kSBuf * kS, kTmO2 = kTmO + kP;
+  static constexpr uint32_t kTmNeed = kTmO2 + kP;
+  static constexpr uint32_t kTmCols = kTmNeed <= 128 ? 128 : kTmNeed <= 256 ? 256 : 512;
+  static_assert(kTmNeed <= 512, "tensor memory columns");
   static constexpr int kPageBytes = kPage * kD * (KV8 ? 1 : 2);
   // a page in shared memory: [8 groups of 8 tokens][3 planes of 64 dims][8 tokens][kRowB], so
   // that 8-token groups are evenly spaced across the pages of a chunk
   static constexpr int kRowB = KV8 ? 64 : 128;
   static constexpr int kPlane = 8 * kRowB;
   static constexpr int kGroup = 3 * kPlane;
-  static constexpr int kStages = KV8 ? 4 : 2;          // chunks per ring
-  static constexpr int kStageBytes = 2 * kPageBytes;
-  // The reference sits kOff binades under the maximum it was taken from and moves when a weight
+  static constexpr int kKStages = KV8 ? (RT == 4 ? 3 : 4) : 2;        // chunks in the K ring
+  static constexpr int kVPages = KV8 ? 8 : (RT == 4 ? 3 : 4);         // pages in the V ring
+  static constexpr int kChunkBytes = 2 * kPageBytes;
+  // P: [16 groups of 8 tokens][atoms][8 tokens][kAtom bytes], swizzled over an atom's rows
+  static constexpr int kPRow = kP * (KV8 ? 1 : 2);
+  static constexpr int kAtom = kPRow % 128 == 0 ? 128 : 64;
+  static constexpr int kPGroup = 8 * kPRow;
+  // Q: [3 planes][kS rows][kRowB]
+  static constexpr int kQPlane = kS * kRowB;
+  // the reference sits kOff binades under the maximum it was taken from and moves when a weight
   // would exceed 2^kTop.  One byte: f16 weights reach 2^15, E5M2 ones go down to 2^-16, so
   // weights of 2^-28 of the largest still count.
   static constexpr float kOff = KV8 ? 12.f : 0.f;
   static constexpr float kTop = KV8 ? 15.f : 8.f;
-  static_assert(kCopies >= 1 && kCopies * kSlots * RT == 8, "128 MMA rows");
   // shared memory (from a 1,024-byte aligned base)
-  static constexpr int kOffV = kStages * kStageBytes;
-  static constexpr int kOffStage = 2 * kStages * kStageBytes; // float [2][128][20]: epilogue; join weights
-  static constexpr int kOffMl = kOffStage + 2 * 128 * 20 * 4; // float [2][128]: references and sums
-  static constexpr int kOffBad = kOffMl + 2 * 128 * 4;        // uint32 [48]: per dim, rows that saw a non-finite value
+  static constexpr int kOffV = kKStages * kChunkBytes;
+  static constexpr int kOffQ = kOffV + kVPages * kPageBytes;
+  static constexpr int kOffP = kOffQ + 3 * kQPlane;                   // (epilogue: weights of the join)
+  static constexpr int kOffCol = kOffP + 16 * kPGroup;                // float [6][kPairs]: per-column values
+  static constexpr int kOffBad = kOffCol + 6 * kPairs * 4;            // uint32 [48]: per dim, rows that saw a non-finite value
   static constexpr int kOffBar = kOffBad + 192;
-  static constexpr int kNumBars = 4 * kStages + 16;
-  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kSmem = kOffMisc + 256 + 1024;
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVPages + 10;
+  static constexpr int kOffMisc = kOffBar + (kNumBars * 8 + 15) / 16 * 16;
+  static constexpr int kSmem = kOffMisc + 128 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+  static_assert(16 * kPGroup >= kMaxJoin * kPairs * 4 && 16 * kPGroup >= kScanSeqs * 4, "P's room is reused");
 };
 
 // ---------------------------------------------------------------- the list of page units
@@ -242,44 +247,70 @@ __device__ __forceinline__ uint32_t float2_to_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&v);
 }
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, float f) {
+  const __half2 v = __hmul2(*reinterpret_cast<__half2 *>(&a), __float2half2_rn(f));
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   const __half2 v = __hsub2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// Q of one MMA row into tensor memory, negated when the scale is negative: bf16 as
-// it is.
-__device__ __forceinline__ void load_q_bf16(const DenseArgs &a, size_t qrow, bool on, uint32_t tq) {
-  const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-  const uint4 *src = reinterpret_cast<const uint4 *>(a.q) + qrow * (kD / 8);
-#pragma unroll
-  for (int x = 0; x < kD / 32; ++x) {
-    uint32_t w[16];
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const uint4 v = on ? ld_cg(src + 4 * x + y) : make_uint4(0, 0, 0, 0);
-      w[4 * y] = v.x ^ flip;
-      w[4 * y + 1] = v.y ^ flip;
-      w[4 * y + 2] = v.z ^ flip;
-      w[4 * y + 3] = v.w ^ flip;
-    }
-    tc::st_16cols(tq + 16 * x, w);
-  }
+// Barrier of the softmax warps (named barrier 1).  They always run the same sequence
+// of these: a warp whose bounded wait expired goes on to the next one, where all learn of it.
+__device__ __forceinline__ bool soft_or(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// D[tmem] (+)= A[smem] * B[smem]^T, one K step; KV8: kind::f8f6f4, else kind::f16.
+template <bool KV8>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, bool accumulate) {
+  if constexpr (KV8) tc::mma_f8(d_tmem, a_desc, b_desc, idesc, accumulate);
+  else tc::mma_bf16(d_tmem, a_desc, b_desc, idesc, accumulate);
 }
 
-// Q of one MMA row as two E4M3 terms (the value and its remainder) of q times a
-// power of two that puts the row's largest magnitude in [2^7, 2^8); returns the
-// inverse of that power.  Two 4-bit terms hold a bf16's 8 bits exactly down to
-// 2^-10 of the largest magnitude; smaller values are rounded to 2^-17 of it.
-__device__ __forceinline__ float load_q_e4m3(const DenseArgs &a, size_t qrow, bool on, uint32_t tq) {
-  const uint4 *src = reinterpret_cast<const uint4 *>(a.q) + qrow * (kD / 8);
-  float top = 0.f;
-  bool finite = true;
-  if (on) {
-#pragma unroll 4
-    for (int x = 0; x < kD / 8; ++x) {
-      const uint4 v = ld_cg(src + x);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// The tile's queries as the N operand, K-major: row j * 16 + h; thread `tid` takes a run of
+// dims of one row.  bf16: as they are.  One byte: two E4M3 terms (rows n and kPairs + n) of q
+// times a power of two that puts the row's largest magnitude in [2^7, 2^8): the nearest code
+// and 16 times the remainder, together a bf16's 8 bits exactly down to 2^-14 of the largest
+// magnitude (smaller values are rounded to multiples of 2^-21 of it).  Returns the factor that
+// scores of the row are to be multiplied by (for every thread of the row).
+template <bool KV8, int RT>
+__device__ __forceinline__ float load_q(const DenseArgs &a, int row0, int nr, int g, uint8_t *sq, int tid) {
+  using C = Cfg<KV8, RT>;
+  constexpr int kPer = kDnSoft / C::kPairs;  // threads per row
+  constexpr int kPieces = kD / 8 / kPer;     // 8-dim pieces per thread
+  const int n = tid / kPer, part = tid % kPer;
+  const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale's sign goes into q
+  const uint4 *src = reinterpret_cast<const uint4 *>(a.q) +
+                     ((size_t)(row0 + n / kHpg) * kHeads + g * kHpg + n % kHpg) * (kD / 8) + part * kPieces;
+  uint4 v[kPieces];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) v[i] = n / kHpg < nr ? ld_cg(src + i) : make_uint4(0, 0, 0, 0);
+  if constexpr (!KV8) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int p = part * kPieces + i;  // dims 8 p ..
+      *reinterpret_cast<uint4 *>(sq + (p >> 3) * C::kQPlane + n * 128 + (((p & 7) ^ (n & 7)) << 4)) =
+          make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
+    }
+    return fabsf(a.scale_log2);
+  } else {
+    float top = 0.f;
+    bool finite = true;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const float f0 = fabsf(bf16lo(w[y])), f1 = fabsf(bf16hi(w[y]));
@@ -287,36 +318,33 @@ __device__ __forceinline__ float load_q_e4m3(const DenseArgs &a, size_t qrow, bo
         top = max3(top, f0, f1);
       }
     }
-  }
-  const int e = (int)(__float_as_uint(top) >> 23);  // biased exponent of the largest magnitude
-  float up = finite ? __uint_as_float((uint32_t)min(261 - e, 254) << 23) : __uint_as_float(0x7FC00000u);
-  if (a.scale_log2 < 0.f) up = -up;
-  const float down = e > 7 ? __uint_as_float((uint32_t)(e - 7) << 23) : __uint_as_float(0x00400000u);
 #pragma unroll
-  for (int x = 0; x < kD / 32; ++x) {
-    uint32_t t0[8], t1[8];
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const uint4 v = on ? ld_cg(src + 4 * x + y) : make_uint4(0, 0, 0, 0);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int z = 0; z < 4; z += 2) {
-        uint32_t c0 = 0, c1 = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t h = float2_to_f16x2(bf16lo(w[z + i]) * up, bf16hi(w[z + i]) * up);
-          const uint32_t c = f16x2_to_e4m3x2(h);
-          c0 |= c << (16 * i);
-          c1 |= f16x2_to_e4m3x2(sub_f16x2(h, e4m3x2_to_f16x2(c))) << (16 * i);
-        }
-        t0[2 * y + z / 2] = c0;
-        t1[2 * y + z / 2] = c1;
-      }
+    for (int o = 1; o < kPer; o <<= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      finite = __shfl_xor_sync(0xffffffffu, (int)finite, o) != 0 && finite;
     }
-    tc::st_8cols(tq + 8 * x, t0);
-    tc::st_8cols(tq + 48 + 8 * x, t1);
+    const int e = (int)(__float_as_uint(top) >> 23);  // biased exponent of the largest magnitude
+    float up = finite ? __uint_as_float((uint32_t)min(261 - e, 254) << 23) : __uint_as_float(0x7FC00000u);
+    const float down = e > 7 ? __uint_as_float((uint32_t)(e - 7) << 23) : __uint_as_float(0x00400000u);
+    if (flip) up = -up;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int p = part * kPieces + i;
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint32_t c0[2] = {0, 0}, c1[2] = {0, 0};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const uint32_t x = float2_to_f16x2(bf16lo(w[y]) * up, bf16hi(w[y]) * up);
+        const uint32_t c = f16x2_to_e4m3x2(x);
+        c0[y >> 1] |= c << (16 * (y & 1));
+        c1[y >> 1] |= f16x2_to_e4m3x2(mul_f16x2(sub_f16x2(x, e4m3x2_to_f16x2(c)), 16.f)) << (16 * (y & 1));
+      }
+      uint8_t *at = sq + (p >> 3) * C::kQPlane + n * 64 + ((((p >> 1) & 3) ^ ((n >> 1) & 3)) << 4) + (p & 1) * 8;
+      *reinterpret_cast<uint2 *>(at) = make_uint2(c0[0], c0[1]);
+      *reinterpret_cast<uint2 *>(at + C::kPairs * 64) = make_uint2(c1[0], c1[1]);
+    }
+    return fabsf(a.scale_log2) * down;
   }
-  return down;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -325,18 +353,20 @@ template <bool KV8, int RT>
 __global__ void __launch_bounds__(kDnThreads, 1)
     dense_kernel(const DenseArgs a, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<KV8, RT>;
-  constexpr int NS = C::kStages, PB = C::kPageBytes, SB = C::kStageBytes, kPairs = RT * kHpg;
+  constexpr int KS = C::kKStages, VP = C::kVPages, PB = C::kPageBytes, NQ = C::kPairs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sk = smem, *sv = smem + C::kOffV;
-  float *stage = reinterpret_cast<float *>(smem + C::kOffStage);
-  float *ml_s = reinterpret_cast<float *>(smem + C::kOffMl);
+  uint8_t *sk = smem, *sv = smem + C::kOffV, *sq = smem + C::kOffQ, *sp = smem + C::kOffP;
+  float *col_s = reinterpret_cast<float *>(smem + C::kOffCol);
+  float *ref_s = col_s, *scale_s = col_s + NQ;                  // reference (0: none yet), score scale
+  float *warp_s = col_s + 2 * NQ;                               // [4][NQ]: the warps' maxima or sums
+  // what a move of the reference changes (thread i reads column i of warp_s, then writes there)
+  float *shift_s = warp_s, *corr_s = warp_s + NQ;
   uint32_t *bad_s = reinterpret_cast<uint32_t *>(smem + C::kOffBad);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
-  uint64_t *k_full = bars, *k_empty = bars + NS, *v_full = bars + 2 * NS, *v_empty = bars + 3 * NS;
-  uint64_t *s_full = bars + 4 * NS, *s_empty = s_full + 1, *p_full = s_full + 2, *p_free = s_full + 3;
-  uint64_t *q_full = s_full + 4, *q_empty = s_full + 5, *o_empty = s_full + 6, *b_soft = s_full + 7,
-           *b_flag = s_full + 8, *b_final = s_full + 9;
+  uint64_t *k_full = bars, *k_empty = bars + KS, *v_full = bars + 2 * KS, *v_empty = v_full + VP;
+  uint64_t *s_full = v_empty + VP, *s_empty = s_full + 2, *p_full = s_full + 4, *p_free = s_full + 5;
+  uint64_t *q_full = s_full + 6, *q_empty = s_full + 7, *o_empty = s_full + 8, *b_final = s_full + 9;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
   int *abort_flag = reinterpret_cast<int *>(smem + C::kOffMisc + 4);
   int *flag_s = reinterpret_cast<int *>(smem + C::kOffMisc + 8);
@@ -344,21 +374,21 @@ __global__ void __launch_bounds__(kDnThreads, 1)
   int *n_bad_s = reinterpret_cast<int *>(smem + C::kOffMisc + 16);
   long long *off_s = reinterpret_cast<long long *>(smem + C::kOffMisc + 24);
   long long *sum_s = reinterpret_cast<long long *>(smem + C::kOffMisc + 32);  // [8]
-  int *bad_list = reinterpret_cast<int *>(stage);                             // [kScanSeqs], before the pipeline runs
+  int *bad_list = reinterpret_cast<int *>(sp);                                // [kScanSeqs], before the pipeline runs
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int i = 0; i < 4 * NS; ++i) mbar_init(bars + i, 1);
-    mbar_init(s_full, 1);
-    mbar_init(s_empty, 4);
+    for (int i = 0; i < 2 * KS + 2 * VP; ++i) mbar_init(bars + i, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(s_empty + i, 4);
+    }
     mbar_init(p_full, 4);
     mbar_init(p_free, 1);
     mbar_init(q_full, 4);
     mbar_init(q_empty, 1);
     mbar_init(o_empty, 4);
-    mbar_init(b_soft, kDnSoft);
-    mbar_init(b_flag, 1);
     mbar_init(b_final, 2);
     *abort_flag = 0;
     *n_bad_s = 0;
@@ -440,7 +470,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       if (base > u0) break;
     }
   }
-  if (warp == 0) tc::tmem_alloc(tmem_slot, kTmCols);
+  if (warp == 0) tc::tmem_alloc(tmem_slot, C::kTmCols);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -448,47 +478,55 @@ __global__ void __launch_bounds__(kDnThreads, 1)
   Walk<RT> walk(a, *start_s, *off_s, u0, count);
   Seg x;
 
+  // Bounded wait by polling: a suspended try_wait resumes some hundred cycles after its phase
+  // completes, and three such waits are on a chunk's chain (S^T, P, the release of their buffers).
   auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-    if (*reinterpret_cast<volatile int *>(abort_flag)) return false;
-    if (mbar_wait_bounded_hint(bar, parity, kDnWaitNs, kDnHintNs)) return true;
-    *reinterpret_cast<volatile int *>(abort_flag) = 1;
-    record_error(a.err, S5_ERR_TIMEOUT, 0);
+    for (int i = 0; i < 64; ++i)
+      if (mbar_test_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!*reinterpret_cast<volatile int *>(abort_flag)) {
+      for (int i = 0; i < 64; ++i)
+        if (mbar_test_wait(bar, parity)) return true;
+      if (globaltimer_ns() - t0 > kDnWaitNs) {
+        *reinterpret_cast<volatile int *>(abort_flag) = 1;
+        record_error(a.err, S5_ERR_TIMEOUT, 0);
+      }
+    }
     return false;
   };
 
   if (warp == kWarpK || warp == kWarpV) {
-    // ---------------- TMA producers ----------------
+    // ---------------- TMA producers: K a chunk at a time, V a page at a time ----------------
     const bool is_k = warp == kWarpK;
-    uint8_t *ring = is_k ? sk : sv;
-    const CUtensorMap *map = is_k ? &tm_k : &tm_v;
-    uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
     const uint64_t policy = a.reread ? policy_evict_normal() : policy_evict_first();
-    int gc = 0;
+    int n = 0;  // chunks (K) or pages (V) so far
     bool ok = true;
     while (ok && walk.next(x)) {
       const int32_t *pt = a.page_table + (size_t)x.s * a.max_pages + x.p0;
       int ids = lane < x.np ? ld_cg(pt + lane) : -1;  // pages c .. c + 31, one per lane; the next 32 in flight
       for (int c = 0; c < x.np && ok; c += 32) {
         const int nxt = c + 32 + lane < x.np ? ld_cg(pt + c + 32 + lane) : -1;
-        const int m = min(32, x.np - c);
-        for (int i = 0; i < m; i += 2, ++gc) {
-          const int page[2] = {__shfl_sync(0xffffffffu, ids, i), __shfl_sync(0xffffffffu, ids, i + 1)};
+        const int m = min(32, x.np - c), step = is_k ? 2 : 1;
+        for (int i = 0; i < m; i += step, ++n) {
+          const int page0 = __shfl_sync(0xffffffffu, ids, i), page1 = __shfl_sync(0xffffffffu, ids, min(i + 1, 31));
           int go = 1;
           if (lane == 0) {
-            const int st = gc % NS;
-            if (gc >= NS) go = wait(empty + st, ((gc / NS) - 1) & 1) ? 1 : 0;
+            const int depth = is_k ? KS : VP, st = n % depth;
+            uint64_t *full = (is_k ? k_full : v_full) + st;
+            if (n >= depth) go = wait((is_k ? k_empty : v_empty) + st, ((n / depth) - 1) & 1) ? 1 : 0;
             if (go) {
-              bool page_ok[2];
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                page_ok[y] = page[y] >= 0 && page[y] < a.num_pages;
-                if (!page_ok[y] && is_k && i + y < m) record_error(a.err, S5_ERR_DEVICE_BOUNDS, x.row0);
+              const bool ok0 = page0 >= 0 && page0 < a.num_pages;
+              if (is_k) {
+                const bool ok1 = i + 1 < m && page1 >= 0 && page1 < a.num_pages;
+                if (!ok0 || (i + 1 < m && !ok1)) record_error(a.err, S5_ERR_DEVICE_BOUNDS, x.row0);
+                mbar_arrive_expect_tx(full, (ok0 ? PB : 0) + (ok1 ? PB : 0));
+                uint8_t *dst = sk + st * C::kChunkBytes;
+                if (ok0) tma_load_4d(dst, &tm_k, 0, 0, 0, (page0 * kKv + x.g) * (kPage / 8), full, policy);
+                if (ok1) tma_load_4d(dst + PB, &tm_k, 0, 0, 0, (page1 * kKv + x.g) * (kPage / 8), full, policy);
+              } else {
+                mbar_arrive_expect_tx(full, ok0 ? PB : 0);
+                if (ok0) tma_load_4d(sv + st * PB, &tm_v, 0, 0, 0, (page0 * kKv + x.g) * (kPage / 8), full, policy);
               }
-              mbar_arrive_expect_tx(full + st, (page_ok[0] ? PB : 0) + (page_ok[1] ? PB : 0));
-#pragma unroll
-              for (int y = 0; y < 2; ++y)
-                if (page_ok[y])
-                  tma_load_4d(ring + st * SB + y * PB, map, 0, 0, 0, (page[y] * kKv + x.g) * (kPage / 8), full + st, policy);
             }
           }
           if (!__shfl_sync(0xffffffffu, go, 0)) {
@@ -500,44 +538,37 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       }
     }
     // no copy may still be writing shared memory when the CTA retires
-    if (lane == 0)
-      for (int c = max(0, gc - NS); c < gc; ++c) mbar_wait_bounded(full + c % NS, (c / NS) & 1, kDnWaitNs);
-  } else if (warp == kWarpS) {
-    // ---------------- S = Q K^T ----------------
     if (lane == 0) {
-      const uint32_t k_base = smem_u32(sk);
+      const int depth = is_k ? KS : VP;
+      for (int c = max(0, n - depth); c < n; ++c)
+        mbar_wait_bounded((is_k ? k_full : v_full) + c % depth, (c / depth) & 1, kDnWaitNs);
+    }
+  } else if (warp == kWarpS) {
+    // ---------------- S^T = K Q^T ----------------
+    if (lane == 0) {
+      constexpr uint32_t idesc = KV8 ? tc::idesc_f8_f32(128, C::kS, 0, 0) : tc::idesc_bf16_f32(128, C::kS);
+      const uint64_t kd0 = tc::smem_desc_sw(smem_u32(sk), 16, C::kGroup, C::kRowB);
+      const uint64_t qd0 = tc::smem_desc_sw(smem_u32(sq), 16, C::kPlane, C::kRowB);
       int gc = 0, qi = 0;
       bool ok = true;
       while (ok && walk.next(x)) {
         if (!wait(q_full, qi & 1)) break;
         for (int c = 0; c < x.np; c += 2, ++gc) {
-          const int st = gc % NS;
-          if (!wait(k_full + st, (gc / NS) & 1) || (gc >= 1 && !wait(s_empty, (gc - 1) & 1))) {
+          const int st = gc % KS, sb = gc % C::kSBuf, use = gc / C::kSBuf;
+          if (!wait(k_full + st, (gc / KS) & 1) || (use >= 1 && !wait(s_empty + sb, (use - 1) & 1))) {
             ok = false;
             break;
           }
           tc::fence_after_sync();
-          const uint32_t kb = k_base + st * SB;
-          const int n = c + 1 < x.np ? 2 * kPage : kPage;  // (a run's last page may stand alone)
-          if constexpr (KV8) {
-            const uint32_t idesc = tc::idesc_f8_f32(128, n, 0, false);
+          const uint64_t kd = kd0 + (uint32_t)(st * (C::kChunkBytes >> 4));
+          // a K step is 32 bytes of a row: 4 (bf16) or 2 (one byte) per plane
+          constexpr int kSteps = KV8 ? 6 : 12, kPer = kSteps / 3;
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int kk = 0; kk < kD / 32; ++kk)
-                tc::mma_f8_ts(tmem + kTmS, tmem + kTmQ + t * 48 + kk * 8,
-                                tc::smem_desc_sw64(kb + (kk >> 1) * C::kPlane + (kk & 1) * 32, 16, C::kGroup), idesc,
-                                t + kk > 0);
-          } else {
-            const uint32_t idesc = tc::idesc_bf16_f32(128, n);
-#pragma unroll
-            for (int kk = 0; kk < kD / 16; ++kk)
-              tc::mma_bf16_ts(tmem + kTmS, tmem + kTmQ + kk * 8,
-                              tc::smem_desc_k_sw128_stride(kb + (kk >> 2) * C::kPlane + (kk & 3) * 32, C::kGroup), idesc,
-                              kk > 0);
-          }
+          for (int kk = 0; kk < kSteps; ++kk)
+            mma_ss<KV8>(tmem + sb * C::kS, kd + (((kk / kPer) * C::kPlane + (kk % kPer) * 32) >> 4),
+                        qd0 + (((kk / kPer) * C::kQPlane + (kk % kPer) * 32) >> 4), idesc, kk > 0);
           tc::commit(k_empty + st);
-          tc::commit(s_full);
+          tc::commit(s_full + sb);
           if (c + 2 >= x.np) tc::commit(q_empty);
         }
         ++qi;
@@ -545,84 +576,66 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       tc::commit(b_final);  // arrives once every MMA issued above has completed
     }
   } else if (warp == kWarpPv) {
-    // ---------------- O += P V ----------------
+    // ---------------- O^T += V^T P^T ----------------
     if (lane == 0) {
-      const uint32_t v_base = smem_u32(sv);
-      int gc = 0, qi = 0;
+      constexpr uint32_t base = (KV8 ? tc::idesc_f8_f32(0, C::kP, 0, 1) : tc::idesc_bf16_f32(0, C::kP)) | tc::kIdescMnA |
+                                tc::kIdescMnB;
+      constexpr uint32_t id1 = base | (128u >> 4) << 24, id2 = base | (64u >> 4) << 24;
+      const uint64_t vd0 = tc::smem_desc_sw(smem_u32(sv), C::kPlane, C::kGroup, C::kRowB);
+      const uint64_t pd0 = tc::smem_desc_sw(smem_u32(sp), 8 * C::kAtom, C::kPGroup, C::kAtom);
+      int gc = 0, vp = 0, qi = 0;  // chunks, V pages, runs so far
       bool ok = true;
       while (ok && walk.next(x)) {
-        for (int c = 0; c < x.np; c += 2, ++gc) {
-          const int st = gc % NS;
-          if (!wait(p_full, gc & 1) || !wait(v_full + st, (gc / NS) & 1) ||
-              (c == 0 && qi > 0 && !wait(o_empty, (qi - 1) & 1))) {
+        for (int c = 0; c < x.np && ok; c += 2, ++gc) {
+          if (!wait(p_full, gc & 1) || (c == 0 && qi > 0 && !wait(o_empty, (qi - 1) & 1))) {
             ok = false;
             break;
           }
-          tc::fence_after_sync();
-          const uint32_t vb = v_base + st * SB, pa = tmem + kTmP;
-          const int m = c + 1 < x.np ? 2 : 1;
-          if constexpr (KV8) {
-            constexpr uint32_t idesc = tc::idesc_f8_f32(128, kD, 1, true);
+          const int m = min(2, x.np - c);  // (a run's last page may stand alone)
+          for (int y = 0; y < m; ++y, ++vp) {
+            const int st = vp % VP;
+            if (!wait(v_full + st, (vp / VP) & 1)) {
+              ok = false;
+              break;
+            }
+            tc::fence_after_sync();
+            constexpr int kSteps = KV8 ? 2 : 4, kGrp = 8 / kSteps;  // K steps of a page, 8-token groups of a step
+            const uint64_t vd = vd0 + (uint32_t)(st * (PB >> 4));
+            const uint64_t pd = pd0 + (uint32_t)(y * (8 * C::kPGroup >> 4));
 #pragma unroll
-            for (int t = 0; t < C::kTerms; ++t)
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                if (ks < 2 * m)
-                  tc::mma_f8_ts(tmem + kTmO, pa + t * 32 + ks * 8,
-                                  tc::smem_desc_sw64(vb + ks * 4 * C::kGroup, C::kPlane, C::kGroup), idesc, c + t + ks > 0);
-          } else {
-            constexpr uint32_t idesc = tc::idesc_bf16_f32_bmn(128, kD);
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              if (ks < 4 * m)
-                tc::mma_bf16_ts(tmem + kTmO, pa + ks * 8,
-                                tc::smem_desc_mn_sw128(vb + ks * 2 * C::kGroup, C::kPlane, C::kGroup), idesc, c + ks > 0);
+            for (int ks = 0; ks < kSteps; ++ks) {
+              const uint64_t vk = vd + (ks * kGrp * C::kGroup >> 4), pk = pd + (ks * kGrp * C::kPGroup >> 4);
+              mma_ss<KV8>(tmem + C::kTmO, vk, pk, id1, c + y + ks > 0);
+              mma_ss<KV8>(tmem + C::kTmO2, vk + (2 * C::kPlane >> 4), pk, id2, c + y + ks > 0);
+            }
+            tc::commit(v_empty + st);
           }
-          tc::commit(v_empty + st);
-          tc::commit(p_free);
+          if (ok) tc::commit(p_free);
         }
         ++qi;
       }
       tc::commit(b_final);
     }
   } else {
-    // ---------------- softmax and epilogue: one thread per MMA row ----------------
-    const int h = tid & 15, j = (tid >> 4) % RT, slot = (tid / kPairs) % C::kSlots, cp = tid / (kPairs * C::kSlots);
-    const int pr = tid % kPairs;  // (row, head) pair of the tile
+    // ---------------- softmax and epilogue: thread tid is token tid of the chunk, then dim tid ----------------
     const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
-    constexpr int TOK = C::kTok;
-    int gc = 0, qi = 0, n_soft = 0, n_flag = 0;
-    bool ok = true;
-    // a warp leaves together: if any lane gave up, all do
-    auto wait_warp = [&](uint64_t *bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, wait(bar, parity));
-    };
-    auto soft_sync = [&]() -> bool {  // the 128 threads of these warps
-      mbar_arrive(b_soft);
-      return wait_warp(b_soft, n_soft++ & 1);
-    };
-    {  // P is zero outside each copy's tokens, for good
-      const uint32_t z[16] = {};
+    int gc = 0, vp = 0, qi = 0;  // chunks, V pages, runs so far
+    bool ok = true;              // this warp's waits so far; all four decide at the barriers
+    while (walk.next(x)) {
+      const int t_last = x.t0 + x.nr - 1;
+      if (qi > 0) ok = wait(q_empty, (qi - 1) & 1) && ok;
+      const float scale = fmaxf(load_q<KV8, RT>(a, x.row0, x.nr, x.g, sq, tid), 1e-37f);
+      // (a scale of 0 must not make a score of -inf NaN)
+      fence_proxy_async_smem();
+      if (tid % (kDnSoft / NQ) == 0) scale_s[tid / (kDnSoft / NQ)] = scale;
+      if (tid < NQ) ref_s[tid] = 0.f;
+      bool had = false;  // (thread i < NQ) column i has a reference
+      if (soft_or(!ok)) break;
+      if (lane == 0) mbar_arrive(q_full);
+      float2 l[NQ / 2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tc::st_16cols(tl + kTmP + 16 * i, z);
-      tc::wait_st();
-    }
-    while (ok && walk.next(x)) {
-      const bool row_ok = j < x.nr;
-      const int t_row = x.t0 + j, t_last = x.t0 + x.nr - 1;
-      float m_ref = -INFINITY, l = 0.f, sl2 = fabsf(a.scale_log2);
-      // (a score of -inf, masked or not, has weight 0 with a scale of 0 too)
-      if (qi > 0 && !wait_warp(q_empty, (qi - 1) & 1)) break;
-      {
-        const size_t qrow = (size_t)(x.row0 + j) * kHeads + x.g * kHpg + h;
-        if constexpr (KV8) sl2 *= load_q_e4m3(a, qrow, row_ok, tl + kTmQ);
-        else load_q_bf16(a, qrow, row_ok, tl + kTmQ);
-        sl2 = fmaxf(sl2, 1e-37f);
-        tc::wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
-      }
+      for (int i = 0; i < NQ / 2; ++i) l[i] = make_float2(0.f, 0.f);
+      bool force = true;  // some column has no reference yet
       const int32_t *pt = a.page_table + (size_t)x.s * a.max_pages + x.p0;
       int ids = -1, nxt = lane < x.np ? ld_cg(pt + lane) : -1;
       for (int c = 0; c < x.np; c += 2, ++gc) {
@@ -635,259 +648,293 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         const bool ok_a = pa >= 0 && pa < a.num_pages, ok_b = pb >= 0 && pb < a.num_pages;
         const int base = (x.p0 + c) * kPage;
         const bool masked = !ok_a || !ok_b || base + kChunk - 1 > x.t0;
-        // tokens 0 .. lim of this thread's run are visible to its row, past the 64th those to lim_b
-        const int lim0 = t_row - base - cp * TOK;
-        const int lim = (TOK == kChunk || cp * TOK < kPage ? ok_a : ok_b) ? lim0 : -1;
-        const int lim_b = ok_b ? lim0 : -1;
-        if (!wait_warp(s_full, gc & 1)) {
-          ok = false;
-          break;
-        }
-        tc::fence_after_sync();
-        uint32_t v[TOK];
-#pragma unroll
-        for (int i = 0; i < TOK / 32; ++i)
-          tc::ld_32cols(tl + kTmS + cp * TOK + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * i));
-        tc::wait_ld();
-        tc::fence_before_sync();
+        const int sb = gc % C::kSBuf;
+        ok = wait(s_full + sb, (gc / C::kSBuf) & 1) && ok;
         __syncwarp();
-        if (lane == 0) mbar_arrive(s_empty);
-        if (masked) {
+        tc::fence_after_sync();
+        // the token's scores, two columns per element
+        float2 sc[NQ / 2];
+        {
+          const uint32_t ts = tl + sb * C::kS;
+          if constexpr (!KV8) {
 #pragma unroll
-          for (int i = 0; i < TOK; ++i)
-            if (i > (i < kPage ? lim : lim_b)) v[i] = 0xFF800000u;  // -inf
-        }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            for (int i = 0; i < NQ / 16; ++i)
+              tc::ld_16cols(ts + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(reinterpret_cast<uint32_t *>(sc) + 16 * i));
+            tc::wait_ld();
+          } else {
 #pragma unroll
-        for (int i = 0; i < TOK; i += 2)
-          mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-        // scores in log2 units are sl2 * S (sl2 >= 0: a negative scale's sign is in Q)
-        const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const float top = raw * sl2;
-        // the reference moves only when a weight would exceed 2^kTop (or with the first finite score)
-        const bool first = m_ref == -INFINITY;
-        const bool grow = first ? top > -INFINITY : top - m_ref > C::kTop;
-        const bool resc = grow && !first;
-        const float m_old = m_ref;
-        if (grow) m_ref = top - C::kOff;
-        if (__any_sync(0xffffffffu, resc)) {
-          const float corr = resc ? hw_exp2(m_old - m_ref) : 1.f;
-          if (c > 0) {  // O holds the chunks before: after their last product
-            if (!wait_warp(p_free, (gc - 1) & 1)) {
-              ok = false;
-              break;
-            }
-            tc::fence_after_sync();
-#pragma unroll 1
-            for (int cb = 0; cb < kD / 16; ++cb) {
-              uint32_t o[16];
-              tc::ld_16cols(tl + kTmO + cb * 16, o);
+            for (int i = 0; i < NQ / 16; ++i) {
+              uint32_t lo[16];
+              tc::ld_16cols(ts + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(reinterpret_cast<uint32_t *>(sc) + 16 * i));
+              tc::ld_16cols(ts + NQ + 16 * i, lo);
               tc::wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
-              tc::st_16cols(tl + kTmO + cb * 16, o);
+              for (int y = 0; y < 8; ++y)
+                sc[8 * i + y] = fma2(make_float2(__uint_as_float(lo[2 * y]), __uint_as_float(lo[2 * y + 1])),
+                                     make_float2(0.0625f, 0.0625f), sc[8 * i + y]);
+            }
+          }
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_empty + sb);
+        if (masked) {
+          const int pos = (tid < kPage ? ok_a : ok_b) ? base + tid : 0x7fffffff;
+#pragma unroll
+          for (int j = 0; j < RT; ++j)
+            if (pos > min(x.t0 + j, t_last))
+#pragma unroll
+              for (int i = 0; i < 8; ++i) sc[8 * j + i] = make_float2(-INFINITY, -INFINITY);
+        }
+        // relative to the references, in log2 units
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < NQ / 2; i += 2) {
+          const float4 r = *reinterpret_cast<const float4 *>(ref_s + 2 * i);
+          float4 w = make_float4(scale, scale, scale, scale);
+          if constexpr (KV8) w = *reinterpret_cast<const float4 *>(scale_s + 2 * i);
+          sc[i] = fma2(sc[i], make_float2(w.x, w.y), make_float2(-r.x, -r.y));
+          sc[i + 1] = fma2(sc[i + 1], make_float2(w.z, w.w), make_float2(-r.z, -r.w));
+          mx[0] = max3(mx[0], sc[i].x, sc[i].y);
+          mx[1] = max3(mx[1], sc[i + 1].x, sc[i + 1].y);
+        }
+        // a reference moves only when a weight would exceed 2^kTop (or with its first finite score)
+        if (soft_or(force || !ok || fmaxf(mx[0], mx[1]) > C::kTop)) {
+          // maxima of the columns over the chunk's tokens
+#pragma unroll
+          for (int i = 0; i < NQ; ++i) {
+            int b = __float_as_int(fmaxf((i & 1) ? sc[i / 2].y : sc[i / 2].x, -INFINITY));  // (NaN: -inf)
+            b = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
+            if (lane == (i & 31)) warp_s[warp * NQ + i] = __int_as_float(b ^ ((b >> 31) & 0x7fffffff));
+          }
+          if (soft_or(!ok)) {
+            ok = false;
+            break;
+          }
+          bool none = false;
+          if (tid < NQ) {
+            const float top = fmaxf(fmaxf(warp_s[tid], warp_s[NQ + tid]), fmaxf(warp_s[2 * NQ + tid], warp_s[3 * NQ + tid]));
+            const bool grow = had ? top > C::kTop : top > -INFINITY;
+            const float shift = grow ? top - C::kOff : 0.f;
+            shift_s[tid] = shift;
+            corr_s[tid] = grow && had ? hw_exp2(-shift) : 1.f;
+            ref_s[tid] += shift;
+            had = had || grow;
+            none = !had;
+          }
+          force = soft_or(none);
+#pragma unroll
+          for (int i = 0; i < NQ / 2; ++i) {
+            const float2 sh = *reinterpret_cast<const float2 *>(shift_s + 2 * i);
+            const float2 co = *reinterpret_cast<const float2 *>(corr_s + 2 * i);
+            sc[i] = add2(sc[i], make_float2(-sh.x, -sh.y));
+            l[i].x *= co.x;
+            l[i].y *= co.y;
+          }
+          if (c > 0) {  // O^T holds the chunks before: after their last product
+            ok = wait(p_free, (gc - 1) & 1) && ok;
+            __syncwarp();
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int cb = 0; cb < 2 * C::kP / 16; ++cb) {
+              uint32_t o[16];
+              tc::ld_16cols(tl + C::kTmO + cb * 16, o);
+              tc::wait_ld();
+              const float *co = corr_s + (cb * 16) % NQ;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * co[i]);
+              tc::st_16cols(tl + C::kTmO + cb * 16, o);
             }
             tc::wait_st();
           }
-          l *= corr;
         }
-        const float mu = (m_ref == -INFINITY) ? 0.f : m_ref;
-        float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // this slot's term of the weights: the upper half (one byte: E5M2 byte) of what the slots
-        // before it, taking the same toward zero, leave
-        uint32_t pk[C::kTerms][TOK / (KV8 ? 4 : 2)];
+        // P, last read by the products of the chunk before
+        if (gc >= 1) ok = wait(p_free, (gc - 1) & 1) && ok;
+        {
+          uint8_t *row = sp + (tid >> 3) * C::kPGroup + (tid & 7) * C::kAtom;
+          const int sw = C::kAtom == 128 ? tid & 7 : (tid >> 1) & 3;
+          constexpr int kPer = C::kAtom / 16;  // 16-byte pieces of an atom's row
+          auto piece = [&](int i) {
+            return reinterpret_cast<uint4 *>(row + (i / kPer) * 8 * C::kAtom + (((i % kPer) ^ sw) << 4));
+          };
+          constexpr int kCols = KV8 ? 16 : 8;  // columns of a piece
 #pragma unroll
-        for (int i = 0; i < TOK; i += KV8 ? 4 : 2) {
-          float2 p2[2];
+          for (int i0 = 0; i0 < NQ; i0 += kCols) {
+            uint32_t w[C::kTerms][4];
 #pragma unroll
-          for (int y = 0; y < (KV8 ? 2 : 1); ++y) {
-            const float2 s2 = fma2(make_float2(__uint_as_float(v[i + 2 * y]), __uint_as_float(v[i + 2 * y + 1])),
-                                   make_float2(sl2, sl2), make_float2(-mu, -mu));
-            p2[y] = make_float2(hw_exp2(s2.x), hw_exp2(s2.y));
-            ps[y ^ ((i >> 1) & 1)] = add2(ps[y ^ ((i >> 1) & 1)], p2[y]);
-          }
-          if constexpr (KV8) {
-            uint32_t r[2] = {float2_to_f16x2(p2[0].x, p2[0].y), float2_to_f16x2(p2[1].x, p2[1].y)};
+            for (int i = 0; i < kCols; i += KV8 ? 4 : 2) {
+              float2 p2[2];
 #pragma unroll
-            for (int y = 0; y < (C::kSlots - 1) * C::kTerms; ++y)
+              for (int y = 0; y < (KV8 ? 2 : 1); ++y) {
+                const int at = (i0 + i) / 2 + y;
+                p2[y] = make_float2(hw_exp2(sc[at].x), hw_exp2(sc[at].y));
+                l[at] = add2(l[at], p2[y]);
+              }
+              if constexpr (KV8) {
+                uint32_t r0 = float2_to_f16x2(p2[0].x, p2[0].y), r1 = float2_to_f16x2(p2[1].x, p2[1].y);
 #pragma unroll
-              for (int z = 0; z < 2; ++z) r[z] = sub_f16x2(r[z], r[z] & (slot * C::kTerms > y ? 0xFF00FF00u : 0u));
-#pragma unroll
-            for (int t = 0; t < C::kTerms; ++t) {
-              pk[t][i / 4] = __byte_perm(r[0], r[1], 0x7531);
-              if (t + 1 < C::kTerms)
-#pragma unroll
-                for (int z = 0; z < 2; ++z) r[z] = sub_f16x2(r[z], r[z] & 0xFF00FF00u);
+                for (int t = 0; t < C::kTerms; ++t) {
+                  if (t == C::kTerms - 1 && C::kTerms < 4) {  // the last term to nearest
+                    r0 += 0x00800080u;
+                    r1 += 0x00800080u;
+                  }
+                  w[t][i / 4] = __byte_perm(r0, r1, 0x7531);
+                  if (t + 1 < C::kTerms) {
+                    r0 = sub_f16x2(r0, r0 & 0xFF00FF00u);
+                    r1 = sub_f16x2(r1, r1 & 0xFF00FF00u);
+                  }
+                }
+              } else {
+                const uint32_t b0 = __float_as_uint(p2[0].x), b1 = __float_as_uint(p2[0].y);
+                const float2 r = fma2(make_float2(__uint_as_float(b0 & 0xFFFF0000u), __uint_as_float(b1 & 0xFFFF0000u)),
+                                      make_float2(-1.f, -1.f), p2[0]);
+                w[0][i / 2] = __byte_perm(b0, b1, 0x7632);
+                w[1][i / 2] = __byte_perm(__float_as_uint(r.x), __float_as_uint(r.y), 0x7632);
+              }
             }
-          } else if constexpr (C::kSlots == 2) {
-            const uint32_t cut = slot ? 0xFFFF0000u : 0u;
-            const float2 r = fma2(make_float2(__uint_as_float(__float_as_uint(p2[0].x) & cut),
-                                              __uint_as_float(__float_as_uint(p2[0].y) & cut)),
-                                  make_float2(-1.f, -1.f), p2[0]);
-            pk[0][i / 2] = __byte_perm(__float_as_uint(r.x), __float_as_uint(r.y), 0x7632);
-          } else {
-            pk[0][i / 2] = pack_bf16(p2[0].x, p2[0].y);
+#pragma unroll
+            for (int t = 0; t < C::kTerms; ++t)
+              *piece((t * NQ + i0) / kCols) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
           }
-        }
-        l += (ps[0].x + ps[1].x) + (ps[0].y + ps[1].y);
-        // P, last read by the product of the chunk before
-        if (gc >= 1 && !wait_warp(p_free, (gc - 1) & 1)) {
-          ok = false;
-          break;
-        }
-        tc::fence_after_sync();
-        constexpr int PC = TOK / (KV8 ? 4 : 2);  // columns of a term
-#pragma unroll
-        for (int t = 0; t < C::kTerms; ++t) {
-          const uint32_t tp = tl + kTmP + t * 32 + cp * PC;
-          if constexpr (PC == 8) tc::st_8cols(tp, *reinterpret_cast<const uint32_t(*)[8]>(pk[t]));
-          else
-#pragma unroll
-            for (int i = 0; i < PC / 16; ++i) tc::st_16cols(tp + 16 * i, *reinterpret_cast<const uint32_t(*)[16]>(pk[t] + 16 * i));
         }
         if (masked) {
           // V of tokens that a row of the tile does not see must not be NaN or infinite (P is 0 there,
           // but 0 * NaN is NaN): tokens that no row sees become zeros; in tokens that some rows see, a
           // value that is not finite becomes zero and is noted for the rows that see it
-          const int st = gc % NS;
-          if (!wait_warp(v_full + st, (gc / NS) & 1)) {
-            ok = false;
-            break;
-          }
-          uint8_t *vb = sv + st * SB;
-          constexpr int kPieces = C::kRowB / 16;  // 16-byte pieces of a token in a plane
-          const int n_tok = c + 1 < x.np ? kChunk : kPage;
-          // from the first token of a bad page, or the first that some row does not see
-          const int first_tok = !ok_a ? 0 : min(max(x.t0 + 1 - base, 0), ok_b ? kChunk : kPage);
-          for (int i = first_tok * 3 * kPieces + tid; i < n_tok * 3 * kPieces; i += kDnSoft) {
-            const int tok = i / (3 * kPieces), y = i % (3 * kPieces), plane = y / kPieces, piece = y % kPieces;
-            uint4 *at = reinterpret_cast<uint4 *>(vb + (tok >> 3) * C::kGroup + plane * C::kPlane + (tok & 7) * C::kRowB +
-                                                  piece * 16);
-            if (!(tok < kPage ? ok_a : ok_b) || base + tok > t_last) {
-              *at = make_uint4(0, 0, 0, 0);
-            } else if (base + tok > x.t0) {
-              const int swz = KV8 ? (tok >> 1) & 3 : tok & 7;
-              const int d0 = plane * 64 + (piece ^ swz) * (KV8 ? 16 : 8);
-              // rows whose position is at least the token's
-              const uint32_t rows = (0xFFu << (base + tok - x.t0)) & 0xFFu;
-              uint32_t w[4] = {at->x, at->y, at->z, at->w};
-              bool hit = false;
+#pragma unroll 1
+          for (int y = 0; y < min(2, x.np - c); ++y) {
+            const int st = (vp + y) % VP, first = base + y * kPage;
+            const bool ok_y = y == 0 ? ok_a : ok_b;
+            if (ok_y && first + kPage - 1 <= x.t0) continue;
+            ok = wait(v_full + st, ((vp + y) / VP) & 1) && ok;
+            uint8_t *vb = sv + st * PB;
+            constexpr int kPieces = C::kRowB / 16;  // 16-byte pieces of a token in a plane
+            const int from = ok_y ? max(x.t0 + 1 - first, 0) : 0;
+            for (int i = from * 3 * kPieces + tid; i < kPage * 3 * kPieces; i += kDnSoft) {
+              const int tok = i / (3 * kPieces), z = i % (3 * kPieces), plane = z / kPieces, pc = z % kPieces;
+              uint4 *at = reinterpret_cast<uint4 *>(vb + (tok >> 3) * C::kGroup + plane * C::kPlane + (tok & 7) * C::kRowB +
+                                                    pc * 16);
+              if (!ok_y || first + tok > t_last) {
+                *at = make_uint4(0, 0, 0, 0);
+              } else {
+                const int d0 = plane * 64 + (pc ^ (KV8 ? (tok >> 1) & 3 : tok & 7)) * (KV8 ? 16 : 8);
+                // rows whose position is at least the token's
+                const uint32_t rows = (0xFFu << (first + tok - x.t0)) & 0xFFu;
+                uint32_t w[4] = {at->x, at->y, at->z, at->w};
+                bool hit = false;
 #pragma unroll
-              for (int e = 0; e < (KV8 ? 16 : 8); ++e) {
-                const int sh = KV8 ? 8 * (e & 3) : 16 * (e & 1);
-                uint32_t &word = w[KV8 ? e >> 2 : e >> 1];
-                const uint32_t bits = word >> sh;
-                if (KV8 ? (bits & 0x7Fu) == 0x7Fu : (bits & 0x7F80u) == 0x7F80u) {
-                  hit = true;
-                  word &= ~((KV8 ? 0xFFu : 0xFFFFu) << sh);
-                  atomicOr(bad_s + (d0 + e) / 4, rows << (8 * ((d0 + e) & 3)));
+                for (int e = 0; e < (KV8 ? 16 : 8); ++e) {
+                  const int sh = KV8 ? 8 * (e & 3) : 16 * (e & 1);
+                  uint32_t &word = w[KV8 ? e >> 2 : e >> 1];
+                  const uint32_t bits = word >> sh;
+                  if (KV8 ? (bits & 0x7Fu) == 0x7Fu : (bits & 0x7F80u) == 0x7F80u) {
+                    hit = true;
+                    word &= ~((KV8 ? 0xFFu : 0xFFFFu) << sh);
+                    atomicOr(bad_s + (d0 + e) / 4, rows << (8 * ((d0 + e) & 3)));
+                  }
                 }
+                if (hit) *at = make_uint4(w[0], w[1], w[2], w[3]);
               }
-              if (hit) *at = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
-          fence_proxy_async_smem();
         }
-        tc::wait_st();
+        vp += min(2, x.np - c);
+        fence_proxy_async_smem();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
       }
-      if (!ok) break;
 
-      // ---- the run's result: copies and slots summed ----
-      ml_s[tid] = m_ref;
-      ml_s[128 + tid] = l;
-      if (!soft_sync()) {
-        ok = false;
-        break;
+      // ---- the run's result ----
+      if (x.np > 0) ok = wait(p_free, (gc - 1) & 1) && ok;
+      // column sums over the warp: halves of the columns are exchanged until a lane has one (NQ = 64: two)
+      {
+        float v[NQ];
+#pragma unroll
+        for (int i = 0; i < NQ / 2; ++i) {
+          v[2 * i] = l[i].x;
+          v[2 * i + 1] = l[i].y;
+        }
+        int n = NQ, at = 0;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+          if (n > 1) {
+            n >>= 1;
+            const bool up = (lane & o) != 0;
+            if (up) at += n;
+#pragma unroll
+            for (int i = 0; i < NQ / 2; ++i)
+              if (i < n) v[i] = (up ? v[i + n] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + n], o);
+          } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+          }
+        }
+        warp_s[warp * NQ + at] = v[0];
+        if constexpr (NQ == 64) warp_s[warp * NQ + at + 1] = v[1];
       }
-      float M = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < C::kCopies; ++i) M = fmaxf(M, ml_s[i * kPairs * C::kSlots + pr]);
-      const float Mu = (M == -INFINITY) ? 0.f : M;
-      float L = 0.f;
-#pragma unroll
-      for (int i = 0; i < C::kCopies; ++i)
-        L += hw_exp2(ml_s[i * kPairs * C::kSlots + pr] - Mu) * ml_s[128 + i * kPairs * C::kSlots + pr];
+      if (soft_or(!ok)) break;
+      tc::fence_after_sync();
       const bool whole = x.np == x.tile_pages;
-      const float own = hw_exp2(m_ref - Mu) * (whole ? (L == 0.f ? 0.f : a.v_scale / L) : 1.f);
       // parts of a tile: CTA index within the tile, its slot of partial results
       const int c_first = whole ? 0 : (int)(x.tile_u / chunk);
       const int n_parts = whole ? 1 : (int)((x.tile_u + x.tile_pages - 1) / chunk) - c_first + 1;
       const int me = whole ? 0 : (int)blockIdx.x - c_first;
       auto part_slot = [&](int i) { return 2 * (c_first + i) + (i == 0 ? 1 : 0); };
-      float *po = a.part_o + (size_t)part_slot(me) * kPairs * kD;
-      if (tid < kPairs && row_ok) {
-        if (whole) {
-          if (a.lse != nullptr)
-            a.lse[(size_t)(x.row0 + j) * kHeads + x.g * kHpg + h] = L == 0.f ? -INFINITY : (M + hw_log2(L)) * kLn2;
-        } else {
-          float *ml = a.part_ml + (size_t)part_slot(me) * 2 * kPairs;
-          ml[pr] = M;
-          ml[kPairs + pr] = L;
+      float *po = a.part_o + (size_t)part_slot(me) * NQ * kD;
+      auto out_row = [&](int q) { return (size_t)(x.row0 + q / kHpg) * kHeads + x.g * kHpg + q % kHpg; };
+      if (tid < NQ) {
+        const float L = (warp_s[tid] + warp_s[NQ + tid]) + (warp_s[2 * NQ + tid] + warp_s[3 * NQ + tid]);
+        const float M = had ? ref_s[tid] : -INFINITY;
+        corr_s[tid] = whole ? (L == 0.f ? 0.f : a.v_scale / L) : 1.f;
+        if (tid / kHpg < x.nr) {
+          if (whole) {
+            if (a.lse != nullptr) a.lse[out_row(tid)] = L == 0.f ? -INFINITY : (M + hw_log2(L)) * kLn2;
+          } else {
+            float *ml = a.part_ml + (size_t)part_slot(me) * 2 * NQ;
+            ml[tid] = M;
+            ml[NQ + tid] = L;
+          }
         }
       }
-      if (!wait_warp(p_free, (gc - 1) & 1)) {
-        ok = false;
-        break;
-      }
-      tc::fence_after_sync();
+      soft_sync();
 #pragma unroll 1
-      for (int cb = 0; cb < kD / 16; ++cb) {
-        float *sg = stage + (cb & 1) * 128 * 20;
-        uint32_t o[16];
-        tc::ld_16cols(tl + kTmO + cb * 16, o);
-        tc::wait_ld();
+      for (int half = 0; half < 2; ++half) {  // dims 0-127, then 128-191 (M = 64: 16 lanes of every warp)
+        const int d = half == 0 ? tid : 128 + warp * 16 + lane;
+        const bool on = half == 0 || lane < 16;
+        const uint32_t nf = on ? bad_s[d >> 2] >> (8 * (d & 3)) : 0;  // bit j: row j saw a value that is not finite
+#pragma unroll 1
+        for (int j = 0; j < x.nr; ++j) {
+          float v[16];
+          uint32_t o[C::kTerms][16];
 #pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<float4 *>(sg + tid * 20 + i) =
-              make_float4(__uint_as_float(o[i]) * own, __uint_as_float(o[i + 1]) * own, __uint_as_float(o[i + 2]) * own,
-                          __uint_as_float(o[i + 3]) * own);
-        if (!soft_sync()) {
-          ok = false;
-          break;
-        }
-        for (int i = tid; i < kPairs * 4; i += kDnSoft) {
-          const int q = i >> 2, d = cb * 16 + (i & 3) * 4, jj = q >> 4;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int t = 0; t < C::kTerms; ++t)
+            tc::ld_16cols(tl + (half == 0 ? C::kTmO : C::kTmO2) + t * NQ + j * 16, o[t]);
+          tc::wait_ld();
 #pragma unroll
-          for (int z = 0; z < C::kCopies * C::kSlots; ++z) {
-            const float4 y = *reinterpret_cast<const float4 *>(sg + (z * kPairs + q) * 20 + (i & 3) * 4);
-            acc.x += y.x;
-            acc.y += y.y;
-            acc.z += y.z;
-            acc.w += y.w;
+          for (int i = 0; i < 16; ++i) {
+            v[i] = __uint_as_float(o[0][i]);
+#pragma unroll
+            for (int t = 1; t < C::kTerms; ++t) v[i] += __uint_as_float(o[t][i]);
+            v[i] *= corr_s[j * 16 + i];
+            if ((nf >> j) & 1u) v[i] = __uint_as_float(0x7FC00000u);
           }
-          const uint32_t nf = bad_s[d / 4] >> jj;  // byte e: dim d + e, bit 0: this row saw a value that is not finite
-          if (nf & 0x01010101u) {
-            if (nf & 1u) acc.x = __uint_as_float(0x7FC00000u);
-            if (nf & 0x100u) acc.y = __uint_as_float(0x7FC00000u);
-            if (nf & 0x10000u) acc.z = __uint_as_float(0x7FC00000u);
-            if (nf & 0x1000000u) acc.w = __uint_as_float(0x7FC00000u);
-          }
-          if (jj < x.nr) {
+          if (on) {
             if (whole) {
-              uint2 w2;
-              w2.x = pack_bf16(acc.x, acc.y);
-              w2.y = pack_bf16(acc.z, acc.w);
-              *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) +
-                                         ((size_t)(x.row0 + jj) * kHeads + x.g * kHpg + (q & 15)) * kD + d) = w2;
+              __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.out) + out_row(j * kHpg) * kD + d;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) out[i * kD] = __float2bfloat16(v[i]);
             } else {
-              *reinterpret_cast<float4 *>(po + (size_t)q * kD + d) = acc;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) po[(size_t)(j * 16 + i) * kD + d] = v[i];
             }
           }
         }
       }
-      if (!ok) break;
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(o_empty);
       ++qi;
-      if (!soft_sync()) {  // bad_s, stage and ml_s are free again
-        ok = false;
-        break;
-      }
+      soft_sync();  // the columns' values and bad_s are free again
       if (tid < 48) bad_s[tid] = 0;
       if (whole) continue;
 
@@ -898,45 +945,36 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         while (gs * gs < n_parts) ++gs;
       }
       const int n_groups = (n_parts + gs - 1) / gs, grp = me / gs;
-      int level = 0;
-      while (true) {
+      for (int level = 0;; ++level) {
         // level 0: the parts of group grp; level 1: the groups
         const int lead = level == 0 ? grp * gs : 0;
         const int n = level == 0 ? min(gs, n_parts - lead) : n_groups;
         __threadfence();
-        mbar_arrive(b_soft);
+        soft_sync();
         if (tid == 0) {
-          int last = 0;
-          if (wait(b_soft, n_soft & 1)) {
-            __threadfence();
-            uint32_t *cnt = a.cnt + (level == 0 ? part_slot(lead) : 2 * (int)gridDim.x + c_first);
-            last = atomicAdd(cnt, 1u) == (uint32_t)n - 1 ? 1 : 0;
-            if (last) atomicExch(cnt, 0u);  // every part has arrived: ready for the next call
-          }
+          __threadfence();
+          uint32_t *cnt = a.cnt + (level == 0 ? part_slot(lead) : 2 * (int)gridDim.x + c_first);
+          const int last = atomicAdd(cnt, 1u) == (uint32_t)n - 1 ? 1 : 0;
+          if (last) atomicExch(cnt, 0u);  // every part has arrived: ready for the next call
           *flag_s = last;
           __threadfence();
-          mbar_arrive(b_flag);
         }
-        ++n_soft;
-        if (!wait_warp(b_flag, n_flag++ & 1)) {
-          ok = false;
-          break;
-        }
+        soft_sync();
         if (!*flag_s) break;
         __threadfence();
         const bool final = level == 1 || n_groups == 1;
         const int step = level == 0 ? 1 : gs;
         // (a group's joined reference and sum lie behind the parts', its joined O in its first part)
         auto ml_of = [&](int i) {
-          return a.part_ml + ((size_t)part_slot(lead + i * step) + (level == 0 ? 0 : 2 * (size_t)gridDim.x)) * 2 * kPairs;
+          return a.part_ml + ((size_t)part_slot(lead + i * step) + (level == 0 ? 0 : 2 * (size_t)gridDim.x)) * 2 * NQ;
         };
-        float *wt = stage;  // [n][kPairs] weights
-        if (tid < kPairs && row_ok) {
+        float *wt = reinterpret_cast<float *>(sp);  // [n][NQ] weights
+        if (tid < x.nr * kHpg) {
           float mv[kMaxJoin], lv[kMaxJoin], top = -INFINITY, sum = 0.f;
 #pragma unroll
           for (int i = 0; i < kMaxJoin; ++i) {
-            mv[i] = i < n ? ld_cg(ml_of(i) + pr) : -INFINITY;
-            lv[i] = i < n ? ld_cg(ml_of(i) + kPairs + pr) : 0.f;
+            mv[i] = i < n ? ld_cg(ml_of(i) + tid) : -INFINITY;
+            lv[i] = i < n ? ld_cg(ml_of(i) + NQ + tid) : 0.f;
           }
 #pragma unroll
           for (int i = 0; i < kMaxJoin; ++i) top = fmaxf(top, mv[i]);
@@ -950,20 +988,16 @@ __global__ void __launch_bounds__(kDnThreads, 1)
           const float inv = final ? (sum == 0.f ? 0.f : a.v_scale / sum) : 1.f;
 #pragma unroll
           for (int i = 0; i < kMaxJoin; ++i)
-            if (i < n) wt[i * kPairs + pr] = mv[i] * inv;
+            if (i < n) wt[i * NQ + tid] = mv[i] * inv;
           if (final) {
-            if (a.lse != nullptr)
-              a.lse[(size_t)(x.row0 + j) * kHeads + x.g * kHpg + h] = sum == 0.f ? -INFINITY : (top + hw_log2(sum)) * kLn2;
+            if (a.lse != nullptr) a.lse[out_row(tid)] = sum == 0.f ? -INFINITY : (top + hw_log2(sum)) * kLn2;
           } else {
-            float *ml = a.part_ml + ((size_t)part_slot(lead) + 2 * (size_t)gridDim.x) * 2 * kPairs;
-            ml[pr] = top;
-            ml[kPairs + pr] = sum;
+            float *ml = a.part_ml + ((size_t)part_slot(lead) + 2 * (size_t)gridDim.x) * 2 * NQ;
+            ml[tid] = top;
+            ml[NQ + tid] = sum;
           }
         }
-        if (!soft_sync()) {
-          ok = false;
-          break;
-        }
+        soft_sync();
         for (int i = tid; i < x.nr * kHpg * (kD / 4); i += kDnSoft) {
           const int q = i / (kD / 4), d = (i % (kD / 4)) * 4;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -973,11 +1007,11 @@ __global__ void __launch_bounds__(kDnThreads, 1)
             for (int z = 0; z < 8; ++z)
               if (z0 + z < n)
                 y[z] = ld_cg(reinterpret_cast<const float4 *>(
-                    a.part_o + ((size_t)part_slot(lead + (z0 + z) * step) * kPairs + q) * kD + d));
+                    a.part_o + ((size_t)part_slot(lead + (z0 + z) * step) * NQ + q) * kD + d));
 #pragma unroll
             for (int z = 0; z < 8; ++z)
               if (z0 + z < n) {
-                const float wz = wt[(z0 + z) * kPairs + q];
+                const float wz = wt[(z0 + z) * NQ + q];
                 acc.x = fmaf(wz, y[z].x, acc.x);
                 acc.y = fmaf(wz, y[z].y, acc.y);
                 acc.z = fmaf(wz, y[z].z, acc.z);
@@ -988,17 +1022,13 @@ __global__ void __launch_bounds__(kDnThreads, 1)
             uint2 w2;
             w2.x = pack_bf16(acc.x, acc.y);
             w2.y = pack_bf16(acc.z, acc.w);
-            *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) +
-                                       ((size_t)(x.row0 + (q >> 4)) * kHeads + x.g * kHpg + (q & 15)) * kD + d) = w2;
+            *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + out_row(q) * kD + d) = w2;
           } else {
-            *reinterpret_cast<float4 *>(a.part_o + ((size_t)part_slot(lead) * kPairs + q) * kD + d) = acc;
+            *reinterpret_cast<float4 *>(a.part_o + ((size_t)part_slot(lead) * NQ + q) * kD + d) = acc;
           }
         }
-        if (final) {
-          if (!soft_sync()) ok = false;  // the weights are read before the next epilogue writes there
-          break;
-        }
-        level = 1;
+        soft_sync();  // the weights are read before P is written there again
+        if (final) break;
       }
     }
   }
@@ -1009,7 +1039,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
   tc::fence_after_sync();
   if (warp == 0) {
     mbar_wait_bounded(b_final, 0, kDnWaitNs);
-    tc::tmem_dealloc(tmem, kTmCols);
+    tc::tmem_dealloc(tmem, C::kTmCols);
   }
 }
 
@@ -1038,7 +1068,6 @@ cudaError_t launch_dense(const DenseArgs &a, const CUtensorMap &tk, const CUtens
     case 1: return launch<false, 1>(a, tk, tv, st);
     case 2: return launch<false, 2>(a, tk, tv, st);
     case 4: return launch<false, 4>(a, tk, tv, st);
-    case 8: return launch<false, 8>(a, tk, tv, st);
     case 17: return launch<true, 1>(a, tk, tv, st);
     case 18: return launch<true, 2>(a, tk, tv, st);
     case 20: return launch<true, 4>(a, tk, tv, st);

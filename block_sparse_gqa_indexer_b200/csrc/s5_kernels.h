@@ -143,8 +143,7 @@ struct TileArgs {
 };
 
 // Dense attention over the whole cache.
-constexpr int kDenseMaxRows = 8;   // query rows per tile (8 rows x 16 heads = M 128), bf16 KV
-constexpr int kDenseMaxRows8 = 4;  // ... one-byte KV (the other half of M holds the weights' lower terms)
+constexpr int kDenseMaxRows = 4;  // query rows per tile (4 rows x 16 heads x 4 terms = N 256)
 
 struct DenseArgs {
   int num_pages;
@@ -159,7 +158,7 @@ struct DenseArgs {
   float scale_log2;  // sm_scale * log2(e) (one-byte KV: times k_scale)
   float v_scale;     // one-byte KV: value of a V code = v_scale * E4M3(code)
   int kv8;           // nonzero: K / V pools hold one-byte E4M3 codes
-  int tile_rows;     // query rows per tile: 1, 2, 4 or (bf16 KV) 8
+  int tile_rows;     // query rows per tile: 1, 2 or 4
   int reread;        // nonzero: sequences may have several tiles, which read the same pages
   int n_ctas;
   void *out;

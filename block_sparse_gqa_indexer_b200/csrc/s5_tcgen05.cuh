@@ -72,6 +72,19 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
   return d;
 }
 
+// Any swizzled operand: `lbo` bytes between groups of one swizzle row's elements
+// along MN (MN-major; unused K-major), `sbo` bytes between groups of 8 rows; rows of
+// 128 bytes (layout type 2) or 64 bytes (4), swizzled over that width.
+__device__ __forceinline__ uint64_t smem_desc_sw(uint32_t saddr, uint32_t lbo, uint32_t sbo, int row_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)(row_bytes == 128 ? 2u : 4u) << 61;
+  return d;
+}
+
 // Instruction descriptor of kind::f16 with bf16 A and B, fp32 accumulate,
 // both operands K-major: c_format F32 [4,6), a/b format BF16 [7,10)/[10,13),
 // N >> 3 [17,23), M >> 4 [24,29).
@@ -84,26 +97,14 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32_bmn(int M, int N) {
   return idesc_bf16_f32(M, N) | (1u << 16);
 }
 
-// K-major and MN-major operands of one-byte elements with the 64-byte swizzle
-// (layout type 4): atoms of 8 rows x 64 bytes, 512 bytes each.  K-major: `sbo`
-// bytes between 8-row atoms.  MN-major: `lbo` bytes between 64-element MN
-// groups, `sbo` bytes between 8-row K groups.
-__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)4u << 61;
-  return d;
-}
-
-// Instruction descriptor of kind::f8f6f4, fp32 accumulate: `a_fmt` the format of
-// A (0: E4M3, 1: E5M2), B E4M3; `b_mn`: B is MN-major.
-__host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, int a_fmt, bool b_mn) {
-  return (1u << 4) | ((uint32_t)a_fmt << 7) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
+// Instruction descriptor of kind::f8f6f4, fp32 accumulate: `a_fmt`, `b_fmt` the
+// formats of A and B (0: E4M3, 1: E5M2).
+__host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, int a_fmt, int b_fmt) {
+  return (1u << 4) | ((uint32_t)a_fmt << 7) | ((uint32_t)b_fmt << 10) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
+// Bits that make A and B MN-major in an instruction descriptor.
+constexpr uint32_t kIdescMnA = 1u << 15, kIdescMnB = 1u << 16;
 
 // ---- MMA ----------------------------------------------------------------------
 // D[tmem] (+)= A[smem] * B[smem]^T for one K=16 step; issued by one thread.
@@ -129,16 +130,14 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
-// One-byte operands, A in tensor memory: M rows (lanes) x 32 elements (8
-// columns, four consecutive K elements per 32-bit column, the lowest K in the
-// low byte); one K=32 step.
-__device__ __forceinline__ void mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            bool accumulate) {
+// D[tmem] (+)= A[smem] * B[smem]^T with one-byte operands (kind::f8f6f4), one K = 32 step.
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
 

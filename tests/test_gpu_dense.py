@@ -5,7 +5,10 @@ Tolerances, derived from the roundings of the computation.  With A = sum_j w_j |
 (the softmax-weighted magnitude of the values) and B = sm_scale * max_j sum_d |q_d K_jd|:
   output rounding        half a bf16 step:               2^-8 |out|
   weights                rounded to bf16 (bf16 KV):      2^-8 A
-                         to terms of 11 bits (one byte): 2^-11 A
+                         one byte, up to 2 rows a sequence: to 11 bits, 2^-11 A; more rows:
+                         three terms of 3 bits.  Two terms cut toward zero leave less than
+                         2^-5 of the weight's power of two, which the third rounds to 3 of
+                         its bits: off by at most 2^-5 / 2 / 2^3 = 2^-9:  2^-9 A
   scores                 192 fp32 products and the scale: every weight off by
                          a factor of at most 1 +- 200 * 2^-24 B + 2^-20 (exp2 of
                          a scaled, shifted score), in the sum and the quotient: twice that, times A
@@ -115,7 +118,7 @@ class Case:
             out, a = term.sum(3), term.abs().sum(3)
         b = mag.masked_fill(~m, 0.0).amax(-1)
         score = 200 * 2.0 ** -24 * b + 2.0 ** -20
-        weight = 2.0 ** -8 if self.kv == "bf16" else 2.0 ** -11
+        weight = 2.0 ** -8 if self.kv == "bf16" else 2.0 ** -11 if max(self.nq) <= 2 else 2.0 ** -9
         tol = 2.0 ** -8 * out.abs() + (weight + 2 * score + 2.0 ** -27 * n + 2.0 ** -20)[..., None] * a + 1e-30
         tol_lse = score + 2.0 ** -20 + 2.0 ** -27 * n + 2.0 ** -23 * lse.abs()
         r = hi - lo
