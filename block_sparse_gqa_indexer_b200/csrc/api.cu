@@ -479,7 +479,7 @@ s5_status workspace_need(const s5_batch_desc *batch, int32_t window, int groups,
 // ---- dense attention over the whole cache ----
 
 struct DenseWs {
-  size_t part_o, part_ml, end;
+  size_t part_o, part_ml, joins, end;
   int tile_rows, n_ctas;
 };
 
@@ -493,7 +493,8 @@ DenseWs dense_ws(const s5_batch_desc *b, int sms) {
   w.n_ctas = (int)(units < sms ? (units < 1 ? 1 : units) : sms);
   w.part_o = kWsFixed;
   w.part_ml = align_up(w.part_o + (size_t)2 * w.n_ctas * w.tile_rows * kHpg * kD * sizeof(float), 256);
-  w.end = align_up(w.part_ml + (size_t)4 * w.n_ctas * 2 * w.tile_rows * kHpg * sizeof(float), 256);
+  w.joins = align_up(w.part_ml + (size_t)2 * w.n_ctas * 2 * w.tile_rows * kHpg * sizeof(float), 256);
+  w.end = align_up(w.joins + (size_t)w.n_ctas * sizeof(int4), 256);
   return w;
 }
 
@@ -554,7 +555,7 @@ s5_status dense_common(const s5_kv_desc *kv, const s5_batch_desc *b, const void 
   a.lse = lse;
   a.part_o = reinterpret_cast<float *>(wsb + w.part_o);
   a.part_ml = reinterpret_cast<float *>(wsb + w.part_ml);
-  a.cnt = reinterpret_cast<uint32_t *>(wsb + kWsHeader);
+  a.joins = reinterpret_cast<int4 *>(wsb + w.joins);
   a.err = reinterpret_cast<int32_t *>(ws);
   return cuda_status(launch_dense(a, tk, tv, stream));
 }

@@ -16,9 +16,10 @@
 // pages up to its last row.  Every CTA (one per SM, persistent) finds its equal
 // share of the list from the device's lengths by prefix sums, so ragged batches
 // balance to within a page and one long sequence spreads over every SM.  A tile
-// that spans CTAs leaves a part per CTA; the last CTA of a group of parts to
-// arrive joins the group, the last group joins the groups (in CTA order, so
-// results do not depend on who is last).
+// that spans CTAs leaves a part per CTA, and a second kernel joins the parts.  (Joined by the last CTA to arrive, in two levels, a tile
+// of 37 parts took 14 us, 4 rows 21 us: two counters' round trips and the parts
+// read by one SM.  The second kernel takes about 4 us, part of it while the first
+// one's last CTAs still run.)
 //
 // One CTA works in chunks of two pages (128 tokens): warp 4 streams K and warp
 // 5 V, one TMA copy per page and KV group, through rings in shared memory; warp 6
@@ -56,7 +57,6 @@ constexpr int kChunk = 2 * kPage;                // tokens
 constexpr int kScanPer = 4;                      // sequences per thread and round of the prefix sums
 constexpr int kScanSeqs = kDnThreads * kScanPer;
 constexpr uint64_t kDnWaitNs = 2000000000ull;    // 2 s per wait
-constexpr int kMaxJoin = 16;                     // parts joined at a time (16 * 16 >= CTAs)
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <bool KV8, int RT>
@@ -78,8 +78,11 @@ struct Cfg {
   static constexpr int kRowB = KV8 ? 64 : 128;
   static constexpr int kPlane = 8 * kRowB;
   static constexpr int kGroup = 3 * kPlane;
-  static constexpr int kKStages = KV8 ? (RT == 4 ? 3 : 4) : 2;        // chunks in the K ring
-  static constexpr int kVPages = KV8 ? 8 : (RT == 4 ? 3 : 4);         // pages in the V ring
+  // Rings of about 170 KB.  Deeper ones do not stream faster but less evenly: with four V pages (bf16)
+  // the first SM ended 32 x 131,072 tokens 180 us before the last and the call took 1.89 ms, with
+  // three 1.83 ms.
+  static constexpr int kKStages = KV8 ? 3 : 2;                        // chunks in the K ring
+  static constexpr int kVPages = KV8 ? 6 : 3;                         // pages in the V ring
   static constexpr int kChunkBytes = 2 * kPageBytes;
   // P: [16 groups of 8 tokens][atoms][8 tokens][kAtom bytes], swizzled over an atom's rows
   static constexpr int kPRow = kP * (KV8 ? 1 : 2);
@@ -95,7 +98,7 @@ struct Cfg {
   // shared memory (from a 1,024-byte aligned base)
   static constexpr int kOffV = kKStages * kChunkBytes;
   static constexpr int kOffQ = kOffV + kVPages * kPageBytes;
-  static constexpr int kOffP = kOffQ + 3 * kQPlane;                   // (epilogue: weights of the join)
+  static constexpr int kOffP = kOffQ + 3 * kQPlane;
   static constexpr int kOffCol = kOffP + 16 * kPGroup;                // float [6][kPairs]: per-column values
   static constexpr int kOffBad = kOffCol + 6 * kPairs * 4;            // uint32 [48]: per dim, rows that saw a non-finite value
   static constexpr int kOffBar = kOffBad + 192;
@@ -103,7 +106,7 @@ struct Cfg {
   static constexpr int kOffMisc = kOffBar + (kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kSmem = kOffMisc + 128 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-  static_assert(16 * kPGroup >= kMaxJoin * kPairs * 4 && 16 * kPGroup >= kScanSeqs * 4, "P's room is reused");
+  static_assert(16 * kPGroup >= kScanSeqs * 4, "the list of bad sequences lies in P's room");
 };
 
 // ---------------------------------------------------------------- the list of page units
@@ -150,6 +153,13 @@ __device__ __forceinline__ long long group_pages(const Seq &q) {  // of one KV g
   return tiles == 1 ? last : full_tile_pages<RT>(q.ctx, tiles - 1) + last;
 }
 
+// Where a CTA's share begins: unit `off` of sequence s.
+struct Start {
+  Seq q;
+  int s;
+  long long off;
+};
+
 // A run of pages of one tile.
 struct Seg {
   int s, g, row0, nr, t0;    // sequence, KV group, first row, rows, position of the first row
@@ -165,12 +175,15 @@ struct Walk {
   int s, g, k, p;
   long long u, rem;
 
-  __device__ Walk(const DenseArgs &args, int s0, long long off, long long u0, long long count)
-      : a(args), s(s0), u(u0), rem(count) {
-    q = load_seq(a, s);
+  // unit u0 is unit `off` of sequence s0
+  __device__ Walk(const DenseArgs &args, const Seq &q0, int s0, long long off, long long u0, long long count)
+      : a(args), q(q0), s(s0), g(0), u(u0), rem(count) {
     const long long per = group_pages<RT>(q);
-    g = (int)(off / per);
-    const long long o = off - g * per;
+    long long o = off;
+    while (o >= per) {
+      o -= per;
+      ++g;
+    }
     int lo = 0, hi = (q.n + RT - 1) / RT;  // the last tile k whose pages before are <= o
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -181,8 +194,7 @@ struct Walk {
     p = (int)(o - full_tile_pages<RT>(q.ctx, k));
   }
 
-  __device__ bool next(Seg &x) {
-    if (rem <= 0) return false;
+  __device__ void run(Seg &x) const {  // the run that starts here
     const int nr = min(RT, q.n - k * RT);
     x.s = s;
     x.g = g;
@@ -193,6 +205,11 @@ struct Walk {
     x.p0 = p;
     x.np = (int)min((long long)(x.tile_pages - p), rem);
     x.tile_u = u - p;
+  }
+
+  __device__ bool next(Seg &x) {
+    if (rem <= 0) return false;
+    run(x);
     u += x.np;
     rem -= x.np;
     p += x.np;
@@ -347,6 +364,59 @@ __device__ __forceinline__ float load_q(const DenseArgs &a, int row0, int nr, in
   }
 }
 
+// The parts of a tile that spans CTAs: its first CTA, their number, and the slot of partial results
+// of the i-th (a CTA's second slot holds the tile that begins in its share and ends behind it).
+struct Parts {
+  int first, n;
+  __device__ int slot(int i) const { return 2 * (first + i) + (i == 0 ? 1 : 0); }
+};
+__device__ __forceinline__ Parts parts_of(const Seg &x, long long chunk) {
+  Parts p;
+  p.first = (int)(x.tile_u / chunk);
+  p.n = (int)((x.tile_u + x.tile_pages - 1) / chunk) - p.first + 1;
+  return p;
+}
+// row of out and lse of the tile's (row, head) pair q
+__device__ __forceinline__ size_t out_row(const Seg &x, int q) {
+  return (size_t)(x.row0 + q / kHpg) * kHeads + x.g * kHpg + q % kHpg;
+}
+
+// V of tokens that a row of the tile does not see must not be NaN or infinite (P is 0 there, but
+// 0 * NaN is NaN): tokens that no row sees (after t_last, or all of a page that is none) become zeros;
+// in tokens that only some rows see (after t0), a value that is not finite becomes zero and is noted
+// in bad_s for the rows that see it.  Positions are relative to the page's first token.
+template <bool KV8, int RT>
+__device__ __forceinline__ void clean_v(uint8_t *vb, uint32_t *bad_s, bool page_ok, int t0, int t_last, int tid) {
+  using C = Cfg<KV8, RT>;
+  constexpr int kPieces = C::kRowB / 16;  // 16-byte pieces of a token in a plane
+  const int from = page_ok ? max(t0 + 1, 0) : 0;
+  for (int i = from * 3 * kPieces + tid; i < kPage * 3 * kPieces; i += kDnSoft) {
+    const int tok = i / (3 * kPieces), z = i % (3 * kPieces), plane = z / kPieces, pc = z % kPieces;
+    uint4 *at = reinterpret_cast<uint4 *>(vb + (tok >> 3) * C::kGroup + plane * C::kPlane + (tok & 7) * C::kRowB + pc * 16);
+    if (!page_ok || tok > t_last) {
+      *at = make_uint4(0, 0, 0, 0);
+    } else {
+      const int d0 = plane * 64 + (pc ^ (KV8 ? (tok >> 1) & 3 : tok & 7)) * (KV8 ? 16 : 8);
+      // rows whose position is at least the token's
+      const uint32_t rows = (0xFFu << (tok - t0)) & 0xFFu;
+      uint32_t w[4] = {at->x, at->y, at->z, at->w};
+      bool hit = false;
+#pragma unroll
+      for (int e = 0; e < (KV8 ? 16 : 8); ++e) {
+        const int sh = KV8 ? 8 * (e & 3) : 16 * (e & 1);
+        uint32_t &word = w[KV8 ? e >> 2 : e >> 1];
+        const uint32_t bits = word >> sh;
+        if (KV8 ? (bits & 0x7Fu) == 0x7Fu : (bits & 0x7F80u) == 0x7F80u) {
+          hit = true;
+          word &= ~((KV8 ? 0xFFu : 0xFFFFu) << sh);
+          atomicOr(bad_s + (d0 + e) / 4, rows << (8 * ((d0 + e) & 3)));
+        }
+      }
+      if (hit) *at = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
 // ---------------------------------------------------------------- the kernel
 
 template <bool KV8, int RT>
@@ -369,11 +439,9 @@ __global__ void __launch_bounds__(kDnThreads, 1)
   uint64_t *q_full = s_full + 6, *q_empty = s_full + 7, *o_empty = s_full + 8, *b_final = s_full + 9;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
   int *abort_flag = reinterpret_cast<int *>(smem + C::kOffMisc + 4);
-  int *flag_s = reinterpret_cast<int *>(smem + C::kOffMisc + 8);
-  int *start_s = reinterpret_cast<int *>(smem + C::kOffMisc + 12);
-  int *n_bad_s = reinterpret_cast<int *>(smem + C::kOffMisc + 16);
-  long long *off_s = reinterpret_cast<long long *>(smem + C::kOffMisc + 24);
-  long long *sum_s = reinterpret_cast<long long *>(smem + C::kOffMisc + 32);  // [8]
+  int *n_bad_s = reinterpret_cast<int *>(smem + C::kOffMisc + 12);
+  Start *start_s = reinterpret_cast<Start *>(smem + C::kOffMisc + 16);
+  long long *sum_s = reinterpret_cast<long long *>(smem + C::kOffMisc + 64);  // [8]
   int *bad_list = reinterpret_cast<int *>(sp);                                // [kScanSeqs], before the pipeline runs
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -392,31 +460,43 @@ __global__ void __launch_bounds__(kDnThreads, 1)
     mbar_init(b_final, 2);
     *abort_flag = 0;
     *n_bad_s = 0;
-    *start_s = -1;
   }
   if (tid < 48) bad_s[tid] = 0;
   fence_mbar_init();
   __syncthreads();
-  pdl_wait();  // (programmatic launch) global memory is read from here on
+  if (warp == kWarpPv) tc::tmem_alloc(tmem_slot, C::kTmCols);
+
+  if (tid == kWarpK * 32) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+  if (tid == kWarpV * 32) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+  pdl_wait();     // (programmatic launch) global memory is read from here on
+  pdl_trigger();  // the joining kernel's CTAs may take the SMs as they become free, and wait there
+  if (tid == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
 
   // ---- this CTA's share: prefix sums of the sequences' page units ----
-  const int rounds = (a.batch + kScanSeqs - 1) / kScanSeqs;
+  const int per = a.batch <= kDnThreads ? 1 : kScanPer;  // sequences per thread
+  const int rounds = (a.batch + kDnThreads * per - 1) / (kDnThreads * per);
   long long total = 0, units[kScanPer], before = 0;
+  Seq seqs[kScanPer];
   auto scan_round = [&](int r, bool report) {  // units[] of this thread's sequences; exclusive prefix in `before`
     long long mine = 0;
+    bool any_bad = false;
 #pragma unroll
     for (int i = 0; i < kScanPer; ++i) {
-      const int s = r * kScanSeqs + tid * kScanPer + i;
-      units[i] = 0;
-      if (s < a.batch) {
-        const Seq q = load_seq(a, s);
-        units[i] = kKv * group_pages<RT>(q);
-        if (q.bad && report && s % (int)gridDim.x == (int)blockIdx.x) {
-          record_error(a.err, S5_ERR_DEVICE_BOUNDS, max(q.lo, 0));
-          bad_list[atomicAdd(n_bad_s, 1)] = s;
-        }
-      }
+      const int s = (r * kDnThreads + tid) * per + i;
+      seqs[i].n = 0;
+      seqs[i].bad = false;
+      if (i < per && s < a.batch) seqs[i] = load_seq(a, s);
+    }
+#pragma unroll
+    for (int i = 0; i < kScanPer; ++i) {
+      const int s = (r * kDnThreads + tid) * per + i;
+      units[i] = kKv * group_pages<RT>(seqs[i]);
       mine += units[i];
+      if (seqs[i].bad && report && s % (int)gridDim.x == (int)blockIdx.x) {
+        record_error(a.err, S5_ERR_DEVICE_BOUNDS, max(seqs[i].lo, 0));
+        bad_list[atomicAdd(n_bad_s, 1)] = s;
+        any_bad = true;
+      }
     }
     long long incl = mine;
 #pragma unroll
@@ -425,7 +505,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       if (lane >= o) incl += v;
     }
     if (lane == 31) sum_s[warp] = incl;
-    __syncthreads();
+    any_bad = __syncthreads_or(any_bad);
     before = incl - mine;
     long long all = 0;
 #pragma unroll
@@ -433,27 +513,29 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       if (w < warp) before += sum_s[w];
       all += sum_s[w];
     }
-    // rows of bad sequences: zeros
-    const int nb = *n_bad_s;
-    for (int b = 0; b < nb; ++b) {
-      const int s = bad_list[b];
-      const int lo = max(ld_cg(a.cu_q + s), 0), hi = min(ld_cg(a.cu_q + s + 1), a.total_q);
-      for (long long i = (long long)lo * kHeads * (kD / 8) + tid; i < (long long)hi * kHeads * (kD / 8); i += kDnThreads)
-        reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(0, 0, 0, 0);
-      if (a.lse != nullptr)
-        for (long long i = (long long)lo * kHeads + tid; i < (long long)hi * kHeads; i += kDnThreads) a.lse[i] = -INFINITY;
+    if (any_bad) {  // rows of bad sequences: zeros
+      const int nb = *n_bad_s;
+      for (int b = 0; b < nb; ++b) {
+        const int s = bad_list[b];
+        const int lo = max(ld_cg(a.cu_q + s), 0), hi = min(ld_cg(a.cu_q + s + 1), a.total_q);
+        for (long long i = (long long)lo * kHeads * (kD / 8) + tid; i < (long long)hi * kHeads * (kD / 8); i += kDnThreads)
+          reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse != nullptr)
+          for (long long i = (long long)lo * kHeads + tid; i < (long long)hi * kHeads; i += kDnThreads) a.lse[i] = -INFINITY;
+      }
+      __syncthreads();
+      if (tid == 0) *n_bad_s = 0;
     }
-    __syncthreads();
-    if (tid == 0) *n_bad_s = 0;
-    __syncthreads();
+    if (rounds > 1) __syncthreads();  // sum_s and the list are written again
     return all;
   };
   for (int r = 0; r < rounds; ++r) total += scan_round(r, true);
-  const long long chunk = max((total + gridDim.x - 1) / gridDim.x, 1LL);
+  const long long chunk =
+      total < (1LL << 31) ? max(((uint32_t)total + gridDim.x - 1) / gridDim.x, 1u) : (total + gridDim.x - 1) / gridDim.x;
   const long long u0 = chunk * blockIdx.x;
-  if (u0 >= total) return;
+  const bool idle = u0 >= total;
   const long long count = min(chunk, total - u0);
-  {
+  if (!idle) {
     long long base = 0;
     for (int r = 0; r < rounds; ++r) {
       const long long all = rounds > 1 ? scan_round(r, false) : total;
@@ -461,8 +543,9 @@ __global__ void __launch_bounds__(kDnThreads, 1)
 #pragma unroll
       for (int i = 0; i < kScanPer; ++i) {
         if (at <= u0 && u0 < at + units[i]) {
-          *start_s = r * kScanSeqs + tid * kScanPer + i;
-          *off_s = u0 - at;
+          start_s->s = (r * kDnThreads + tid) * per + i;
+          start_s->off = u0 - at;
+          start_s->q = seqs[i];
         }
         at += units[i];
       }
@@ -470,12 +553,15 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       if (base > u0) break;
     }
   }
-  if (warp == 0) tc::tmem_alloc(tmem_slot, C::kTmCols);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  Walk<RT> walk(a, *start_s, *off_s, u0, count);
+  if (idle) {
+    if (warp == kWarpPv) tc::tmem_dealloc(tmem, C::kTmCols);
+    return;
+  }
+  Walk<RT> walk(a, start_s->q, start_s->s, start_s->off, u0, count);
   Seg x;
 
   // Bounded wait by polling: a suspended try_wait resumes some hundred cycles after its phase
@@ -630,7 +716,10 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       if (tid % (kDnSoft / NQ) == 0) scale_s[tid / (kDnSoft / NQ)] = scale;
       if (tid < NQ) ref_s[tid] = 0.f;
       bool had = false;  // (thread i < NQ) column i has a reference
-      if (soft_or(!ok)) break;
+      if (soft_or(!ok)) {
+        ok = false;
+        break;
+      }
       if (lane == 0) mbar_arrive(q_full);
       float2 l[NQ / 2];
 #pragma unroll
@@ -798,44 +887,14 @@ __global__ void __launch_bounds__(kDnThreads, 1)
           }
         }
         if (masked) {
-          // V of tokens that a row of the tile does not see must not be NaN or infinite (P is 0 there,
-          // but 0 * NaN is NaN): tokens that no row sees become zeros; in tokens that some rows see, a
-          // value that is not finite becomes zero and is noted for the rows that see it
+          // V of tokens that a row of the tile does not see must not be NaN or infinite
 #pragma unroll 1
           for (int y = 0; y < min(2, x.np - c); ++y) {
             const int st = (vp + y) % VP, first = base + y * kPage;
             const bool ok_y = y == 0 ? ok_a : ok_b;
             if (ok_y && first + kPage - 1 <= x.t0) continue;
             ok = wait(v_full + st, ((vp + y) / VP) & 1) && ok;
-            uint8_t *vb = sv + st * PB;
-            constexpr int kPieces = C::kRowB / 16;  // 16-byte pieces of a token in a plane
-            const int from = ok_y ? max(x.t0 + 1 - first, 0) : 0;
-            for (int i = from * 3 * kPieces + tid; i < kPage * 3 * kPieces; i += kDnSoft) {
-              const int tok = i / (3 * kPieces), z = i % (3 * kPieces), plane = z / kPieces, pc = z % kPieces;
-              uint4 *at = reinterpret_cast<uint4 *>(vb + (tok >> 3) * C::kGroup + plane * C::kPlane + (tok & 7) * C::kRowB +
-                                                    pc * 16);
-              if (!ok_y || first + tok > t_last) {
-                *at = make_uint4(0, 0, 0, 0);
-              } else {
-                const int d0 = plane * 64 + (pc ^ (KV8 ? (tok >> 1) & 3 : tok & 7)) * (KV8 ? 16 : 8);
-                // rows whose position is at least the token's
-                const uint32_t rows = (0xFFu << (first + tok - x.t0)) & 0xFFu;
-                uint32_t w[4] = {at->x, at->y, at->z, at->w};
-                bool hit = false;
-#pragma unroll
-                for (int e = 0; e < (KV8 ? 16 : 8); ++e) {
-                  const int sh = KV8 ? 8 * (e & 3) : 16 * (e & 1);
-                  uint32_t &word = w[KV8 ? e >> 2 : e >> 1];
-                  const uint32_t bits = word >> sh;
-                  if (KV8 ? (bits & 0x7Fu) == 0x7Fu : (bits & 0x7F80u) == 0x7F80u) {
-                    hit = true;
-                    word &= ~((KV8 ? 0xFFu : 0xFFFFu) << sh);
-                    atomicOr(bad_s + (d0 + e) / 4, rows << (8 * ((d0 + e) & 3)));
-                  }
-                }
-                if (hit) *at = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            }
+            clean_v<KV8, RT>(sv + st * PB, bad_s, ok_y, x.t0 - first, t_last - first, tid);
           }
         }
         vp += min(2, x.np - c);
@@ -872,27 +931,28 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         warp_s[warp * NQ + at] = v[0];
         if constexpr (NQ == 64) warp_s[warp * NQ + at + 1] = v[1];
       }
-      if (soft_or(!ok)) break;
+      if (soft_or(!ok)) {
+        ok = false;
+        break;
+      }
       tc::fence_after_sync();
       const bool whole = x.np == x.tile_pages;
-      // parts of a tile: CTA index within the tile, its slot of partial results
-      const int c_first = whole ? 0 : (int)(x.tile_u / chunk);
-      const int n_parts = whole ? 1 : (int)((x.tile_u + x.tile_pages - 1) / chunk) - c_first + 1;
-      const int me = whole ? 0 : (int)blockIdx.x - c_first;
-      auto part_slot = [&](int i) { return 2 * (c_first + i) + (i == 0 ? 1 : 0); };
-      float *po = a.part_o + (size_t)part_slot(me) * NQ * kD;
-      auto out_row = [&](int q) { return (size_t)(x.row0 + q / kHpg) * kHeads + x.g * kHpg + q % kHpg; };
+      const Parts parts = parts_of(x, chunk);
+      const size_t my_slot = parts.slot((int)blockIdx.x - parts.first);
+      float *po = a.part_o + my_slot * NQ * kD;
       if (tid < NQ) {
         const float L = (warp_s[tid] + warp_s[NQ + tid]) + (warp_s[2 * NQ + tid] + warp_s[3 * NQ + tid]);
         const float M = had ? ref_s[tid] : -INFINITY;
         corr_s[tid] = whole ? (L == 0.f ? 0.f : a.v_scale / L) : 1.f;
         if (tid / kHpg < x.nr) {
           if (whole) {
-            if (a.lse != nullptr) a.lse[out_row(tid)] = L == 0.f ? -INFINITY : (M + hw_log2(L)) * kLn2;
+            if (a.lse != nullptr) a.lse[out_row(x, tid)] = L == 0.f ? -INFINITY : (M + hw_log2(L)) * kLn2;
           } else {
-            float *ml = a.part_ml + (size_t)part_slot(me) * 2 * NQ;
+            float *ml = a.part_ml + my_slot * 2 * NQ;
             ml[tid] = M;
             ml[NQ + tid] = L;
+            // the CTA where a tile begins tells the joining kernel about it
+            if (tid == 0 && parts.first == (int)blockIdx.x) a.joins[blockIdx.x] = make_int4(parts.n, x.row0, x.nr, x.g);
           }
         }
       }
@@ -920,7 +980,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
           }
           if (on) {
             if (whole) {
-              __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.out) + out_row(j * kHpg) * kD + d;
+              __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.out) + out_row(x, j * kHpg) * kD + d;
 #pragma unroll
               for (int i = 0; i < 16; ++i) out[i * kD] = __float2bfloat16(v[i]);
             } else {
@@ -936,100 +996,6 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       ++qi;
       soft_sync();  // the columns' values and bad_s are free again
       if (tid < 48) bad_s[tid] = 0;
-      if (whole) continue;
-
-      // ---- join the tile's parts: groups of `gs` consecutive CTAs, then the groups ----
-      int gs = n_parts;
-      if (n_parts > 8) {
-        gs = 3;
-        while (gs * gs < n_parts) ++gs;
-      }
-      const int n_groups = (n_parts + gs - 1) / gs, grp = me / gs;
-      for (int level = 0;; ++level) {
-        // level 0: the parts of group grp; level 1: the groups
-        const int lead = level == 0 ? grp * gs : 0;
-        const int n = level == 0 ? min(gs, n_parts - lead) : n_groups;
-        __threadfence();
-        soft_sync();
-        if (tid == 0) {
-          __threadfence();
-          uint32_t *cnt = a.cnt + (level == 0 ? part_slot(lead) : 2 * (int)gridDim.x + c_first);
-          const int last = atomicAdd(cnt, 1u) == (uint32_t)n - 1 ? 1 : 0;
-          if (last) atomicExch(cnt, 0u);  // every part has arrived: ready for the next call
-          *flag_s = last;
-          __threadfence();
-        }
-        soft_sync();
-        if (!*flag_s) break;
-        __threadfence();
-        const bool final = level == 1 || n_groups == 1;
-        const int step = level == 0 ? 1 : gs;
-        // (a group's joined reference and sum lie behind the parts', its joined O in its first part)
-        auto ml_of = [&](int i) {
-          return a.part_ml + ((size_t)part_slot(lead + i * step) + (level == 0 ? 0 : 2 * (size_t)gridDim.x)) * 2 * NQ;
-        };
-        float *wt = reinterpret_cast<float *>(sp);  // [n][NQ] weights
-        if (tid < x.nr * kHpg) {
-          float mv[kMaxJoin], lv[kMaxJoin], top = -INFINITY, sum = 0.f;
-#pragma unroll
-          for (int i = 0; i < kMaxJoin; ++i) {
-            mv[i] = i < n ? ld_cg(ml_of(i) + tid) : -INFINITY;
-            lv[i] = i < n ? ld_cg(ml_of(i) + NQ + tid) : 0.f;
-          }
-#pragma unroll
-          for (int i = 0; i < kMaxJoin; ++i) top = fmaxf(top, mv[i]);
-          const float tu = (top == -INFINITY) ? 0.f : top;
-#pragma unroll
-          for (int i = 0; i < kMaxJoin; ++i)
-            if (i < n) {
-              mv[i] = hw_exp2(mv[i] - tu);
-              sum += mv[i] * lv[i];
-            }
-          const float inv = final ? (sum == 0.f ? 0.f : a.v_scale / sum) : 1.f;
-#pragma unroll
-          for (int i = 0; i < kMaxJoin; ++i)
-            if (i < n) wt[i * NQ + tid] = mv[i] * inv;
-          if (final) {
-            if (a.lse != nullptr) a.lse[out_row(tid)] = sum == 0.f ? -INFINITY : (top + hw_log2(sum)) * kLn2;
-          } else {
-            float *ml = a.part_ml + ((size_t)part_slot(lead) + 2 * (size_t)gridDim.x) * 2 * NQ;
-            ml[tid] = top;
-            ml[NQ + tid] = sum;
-          }
-        }
-        soft_sync();
-        for (int i = tid; i < x.nr * kHpg * (kD / 4); i += kDnSoft) {
-          const int q = i / (kD / 4), d = (i % (kD / 4)) * 4;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int z0 = 0; z0 < n; z0 += 8) {
-            float4 y[8];
-#pragma unroll
-            for (int z = 0; z < 8; ++z)
-              if (z0 + z < n)
-                y[z] = ld_cg(reinterpret_cast<const float4 *>(
-                    a.part_o + ((size_t)part_slot(lead + (z0 + z) * step) * NQ + q) * kD + d));
-#pragma unroll
-            for (int z = 0; z < 8; ++z)
-              if (z0 + z < n) {
-                const float wz = wt[(z0 + z) * NQ + q];
-                acc.x = fmaf(wz, y[z].x, acc.x);
-                acc.y = fmaf(wz, y[z].y, acc.y);
-                acc.z = fmaf(wz, y[z].z, acc.z);
-                acc.w = fmaf(wz, y[z].w, acc.w);
-              }
-          }
-          if (final) {
-            uint2 w2;
-            w2.x = pack_bf16(acc.x, acc.y);
-            w2.y = pack_bf16(acc.z, acc.w);
-            *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + out_row(q) * kD + d) = w2;
-          } else {
-            *reinterpret_cast<float4 *>(a.part_o + ((size_t)part_slot(lead) * NQ + q) * kD + d) = acc;
-          }
-        }
-        soft_sync();  // the weights are read before P is written there again
-        if (final) break;
-      }
     }
   }
 
@@ -1037,16 +1003,172 @@ __global__ void __launch_bounds__(kDnThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 0) {
+  if (warp == kWarpPv) {
     mbar_wait_bounded(b_final, 0, kDnWaitNs);
     tc::tmem_dealloc(tmem, C::kTmCols);
+  }
+}
+
+// ---------------------------------------------------------------- the joining kernel
+
+// Work items: of a tile of at most kFewParts parts four (row, head) pairs, a warp each; of a tile of more
+// parts one pair, whose parts the CTA's warps share (warp w takes parts w, w + 4, ...; their sums are
+// added in warp order).  Few parts come with many tiles and many parts with few tiles, so either way the
+// SMs have enough items and a few rounds of loads end each.
+constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32, kJoinCtasPerSm = 6;
+constexpr int kFewParts = 4, kMaxCtas = 256;
+static_assert(kMaxCtas == 2 * kJoinThreads, "two records per thread");
+
+__device__ __forceinline__ void store_joined(const DenseArgs &a, size_t row, int lane, const float2 (&o)[3], float top,
+                                             float sum) {
+  const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
+#pragma unroll
+  for (int e = 0; e < 3; ++e)
+    reinterpret_cast<uint32_t *>(a.out)[row * (kD / 2) + lane + 32 * e] = pack_bf16(o[e].x * inv, o[e].y * inv);
+  if (lane == 0 && a.lse != nullptr) a.lse[row] = sum == 0.f ? -INFINITY : (top + hw_log2(sum)) * kLn2;
+}
+
+template <int RT>
+__global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) dense_join_kernel(const DenseArgs a) {
+  constexpr int NQ = RT * kHpg;
+  __shared__ int4 rec_s[kMaxCtas];
+  __shared__ int first_s[kMaxCtas + 1];  // first item of a CTA's tile
+  __shared__ int sum_s[kJoinWarps];
+  __shared__ float w_s[kMaxCtas], red_s[2][kJoinWarps];
+  __shared__ float2 acc_s[kJoinWarps][kD / 2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  int items[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = 2 * tid + i;
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (c < a.n_ctas) r = ld_cg(reinterpret_cast<const uint4 *>(a.joins + c));
+    rec_s[c] = make_int4((int)r.x, (int)r.y, (int)r.z, (int)r.w);
+    items[i] = r.x == 0 ? 0 : (int)r.z * (r.x <= kFewParts ? kHpg / kJoinWarps : kHpg);
+  }
+  int incl = items[0] + items[1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sum_s[warp] = incl;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w)
+    if (w < warp) incl += sum_s[w];
+  first_s[2 * tid + 1] = incl - items[1];
+  first_s[2 * tid + 2] = incl;
+  if (tid == 0) first_s[0] = 0;
+  __syncthreads();
+  const int total = first_s[kMaxCtas];
+  for (int it = blockIdx.x; it < total; it += gridDim.x) {
+    int c = 0;  // the last c with first_s[c] <= it: its tile has the item
+#pragma unroll
+    for (int o = kMaxCtas / 2; o >= 1; o >>= 1)
+      if (first_s[c + o] <= it) c += o;
+    const int n = rec_s[c].x, row0 = rec_s[c].y, g = rec_s[c].w, i0 = it - first_s[c];
+    const Parts parts{c, n};
+    if (n <= kFewParts) {
+      const int q = i0 * kJoinWarps + warp;
+      float m[kFewParts], l[kFewParts], top = -INFINITY, sum = 0.f;
+      float2 v[kFewParts][3], o[3] = {};
+#pragma unroll
+      for (int i = 0; i < kFewParts; ++i) {
+        m[i] = -INFINITY;
+        if (i < n) {
+          const float *ml = a.part_ml + (size_t)parts.slot(i) * 2 * NQ + q;
+          m[i] = ld_cg(ml);
+          l[i] = ld_cg(ml + NQ);
+          const float *src = a.part_o + ((size_t)parts.slot(i) * NQ + q) * kD + 2 * lane;
+#pragma unroll
+          for (int e = 0; e < 3; ++e) v[i][e] = ld_cg2(src + 64 * e);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kFewParts; ++i) top = fmaxf(top, m[i]);
+      const float tu = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int i = 0; i < kFewParts; ++i)
+        if (i < n) {
+          const float w = hw_exp2(m[i] - tu);
+          sum = fmaf(w, l[i], sum);
+#pragma unroll
+          for (int e = 0; e < 3; ++e) o[e] = fma2(make_float2(w, w), v[i][e], o[e]);
+        }
+      store_joined(a, (size_t)(row0 + q / kHpg) * kHeads + g * kHpg + q % kHpg, lane, o, top, sum);
+    } else {
+      const int q = i0;
+      float m[2], l[2], top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int p = tid + i * kJoinThreads;
+        const float *ml = a.part_ml + (size_t)parts.slot(p) * 2 * NQ + q;
+        m[i] = p < n ? ld_cg(ml) : -INFINITY;
+        l[i] = p < n ? ld_cg(ml + NQ) : 0.f;
+        top = fmaxf(top, m[i]);
+      }
+      float2 o[3] = {};
+      for (int p0 = warp; p0 < n; p0 += 8 * kJoinWarps) {
+        float2 v[8][3];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (p0 + i * kJoinWarps < n) {
+            const float *src = a.part_o + ((size_t)parts.slot(p0 + i * kJoinWarps) * NQ + q) * kD + 2 * lane;
+#pragma unroll
+            for (int e = 0; e < 3; ++e) v[i][e] = ld_cg2(src + 64 * e);
+          }
+        if (p0 == warp) {  // (every warp has a part: n > kFewParts) the weights, while the first parts come
+#pragma unroll
+          for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+          if (lane == 0) red_s[0][warp] = top;
+          __syncthreads();
+#pragma unroll
+          for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, red_s[0][w]);
+          const float tu = top == -INFINITY ? 0.f : top;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float w = hw_exp2(m[i] - tu);
+            w_s[tid + i * kJoinThreads] = w;
+            sum = fmaf(w, l[i], sum);
+          }
+#pragma unroll
+          for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+          if (lane == 0) red_s[1][warp] = sum;
+          __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (p0 + i * kJoinWarps < n) {
+            const float w = w_s[p0 + i * kJoinWarps];
+#pragma unroll
+            for (int e = 0; e < 3; ++e) o[e] = fma2(make_float2(w, w), v[i][e], o[e]);
+          }
+      }
+#pragma unroll
+      for (int e = 0; e < 3; ++e) acc_s[warp][lane + 32 * e] = o[e];
+      __syncthreads();
+      if (warp == 0) {
+        sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+          sum += red_s[1][w];
+          if (w > 0)
+#pragma unroll
+            for (int e = 0; e < 3; ++e) o[e] = add2(o[e], acc_s[w][lane + 32 * e]);
+        }
+        store_joined(a, (size_t)(row0 + q / kHpg) * kHeads + g * kHpg + q % kHpg, lane, o, top, sum);
+      }
+      __syncthreads();  // the shared arrays are written again
+    }
   }
 }
 
 template <bool KV8, int RT>
 cudaError_t launch(const DenseArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t st) {
   auto kernel = dense_kernel<KV8, RT>;
-  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), Cfg<KV8, RT>::kSmem);
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), Cfg<KV8, RT>::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.n_ctas);
@@ -1058,7 +1180,12 @@ cudaError_t launch(const DenseArgs &a, const CUtensorMap &tk, const CUtensorMap 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, tk, tv);
+  e = cudaLaunchKernelEx(&cfg, kernel, a, tk, tv);
+  if (e != cudaSuccess || a.n_ctas == 1) return e;
+  cfg.gridDim = dim3((unsigned)(a.n_ctas * kJoinCtasPerSm));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, dense_join_kernel<RT>, a);
 }
 
 }  // namespace

@@ -66,6 +66,12 @@ __device__ __forceinline__ float4 ld_cg(const float4 *p) {
   return v;
 }
 
+__device__ __forceinline__ float2 ld_cg2(const float *p) {  // 8-byte aligned
+  float2 v;
+  asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+  return v;
+}
+
 struct ErrRec {
   int32_t code;
   int32_t info;

@@ -164,8 +164,8 @@ struct DenseArgs {
   void *out;
   float *lse;
   float *part_o;   // [2 * n_ctas][tile_rows * 16][192]
-  float *part_ml;  // [4 * n_ctas][2][tile_rows * 16]: reference (log2) and sum of a part; joined parts behind
-  uint32_t *cnt;   // [3 * n_ctas] arrival counters, zero between calls
+  float *part_ml;  // [2 * n_ctas][2][tile_rows * 16]: reference (log2) and sum of a part
+  int4 *joins;     // [n_ctas]: parts, first row, rows and KV group of the split tile that begins in a CTA's share
   int32_t *err;
 };
 cudaError_t launch_dense(const DenseArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t st);
