@@ -530,8 +530,10 @@ __global__ void __launch_bounds__(kDnThreads, 1)
     return all;
   };
   for (int r = 0; r < rounds; ++r) total += scan_round(r, true);
-  const long long chunk =
-      total < (1LL << 31) ? max(((uint32_t)total + gridDim.x - 1) / gridDim.x, 1u) : (total + gridDim.x - 1) / gridDim.x;
+  long long chunk = total < (1LL << 31) ? max(((uint32_t)total + gridDim.x - 1) / gridDim.x, 1u)
+                                        : (total + gridDim.x - 1) / gridDim.x;
+  // (short shares take as long for a page as for a chunk, and have fewer parts to join)
+  if (chunk < 16) chunk += chunk & 1;
   const long long u0 = chunk * blockIdx.x;
   const bool idle = u0 >= total;
   const long long count = min(chunk, total - u0);
@@ -707,20 +709,26 @@ __global__ void __launch_bounds__(kDnThreads, 1)
     const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
     int gc = 0, vp = 0, qi = 0;  // chunks, V pages, runs so far
     bool ok = true;              // this warp's waits so far; all four decide at the barriers
-    while (walk.next(x)) {
-      const int t_last = x.t0 + x.nr - 1;
-      if (qi > 0) ok = wait(q_empty, (qi - 1) & 1) && ok;
-      const float scale = fmaxf(load_q<KV8, RT>(a, x.row0, x.nr, x.g, sq, tid), 1e-37f);
+    // Q of a run, once the products of the run before have read theirs
+    float scale = 0.f;
+    auto stage_q = [&](const Seg &y) {
+      scale = fmaxf(load_q<KV8, RT>(a, y.row0, y.nr, y.g, sq, tid), 1e-37f);
       // (a scale of 0 must not make a score of -inf NaN)
       fence_proxy_async_smem();
       if (tid % (kDnSoft / NQ) == 0) scale_s[tid / (kDnSoft / NQ)] = scale;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    };
+    walk.run(x);
+    stage_q(x);
+    while (walk.next(x)) {
+      const int t_last = x.t0 + x.nr - 1;
       if (tid < NQ) ref_s[tid] = 0.f;
       bool had = false;  // (thread i < NQ) column i has a reference
       if (soft_or(!ok)) {
         ok = false;
         break;
       }
-      if (lane == 0) mbar_arrive(q_full);
       float2 l[NQ / 2];
 #pragma unroll
       for (int i = 0; i < NQ / 2; ++i) l[i] = make_float2(0.f, 0.f);
@@ -905,7 +913,12 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       }
 
       // ---- the run's result ----
-      if (x.np > 0) ok = wait(p_free, (gc - 1) & 1) && ok;
+      if (walk.rem > 0) {  // the next run's Q first, so that its first scores are there after this epilogue
+        ok = wait(q_empty, qi & 1) && ok;
+        Seg y;
+        walk.run(y);
+        stage_q(y);
+      }
       // column sums over the warp: halves of the columns are exchanged until a lane has one (NQ = 64: two)
       {
         float v[NQ];
@@ -931,6 +944,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         warp_s[warp * NQ + at] = v[0];
         if constexpr (NQ == 64) warp_s[warp * NQ + at + 1] = v[1];
       }
+      ok = wait(p_free, (gc - 1) & 1) && ok;
       if (soft_or(!ok)) {
         ok = false;
         break;

@@ -120,17 +120,24 @@ def _check(code: int, where: str):
         raise S5Error(code, where)
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+# (A small call is bound by the host: the helpers below hand plain integers to
+# ctypes, take the current stream's handle without building a Stream object,
+# which takes 3 us, and pass good arguments in one expression.)
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _need(t: torch.Tensor, dtype, name: str, shape=None):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous() and (
+            shape is None or t.shape == shape):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -369,19 +376,28 @@ def s5_append_kv_fp8(k_pool, v_pool, key_pool, batch: Batch, k_new, v_new, key_n
                                  ws.numel(), _stream(stream)), "s5_append_kv_fp8")
 
 
-def _dense_args(batch: Batch, q, out, lse, ws):
+def _same_device(*tensors):
+    """The kernels run on the current device: every tensor has to be there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
+def _dense_args(k_pool, v_pool, batch: Batch, q, out, lse, ws):
     _need(q, torch.bfloat16, "q", (batch.total_q, N_HEADS, HEAD_DIM))
     _need(out, torch.bfloat16, "out", (batch.total_q, N_HEADS, HEAD_DIM))
     if lse is not None:
         _need(lse, torch.float32, "lse", (batch.total_q, N_HEADS))
     _need(ws, torch.uint8, "ws")
+    _same_device(k_pool, v_pool, batch.page_table, q, out, lse, ws)
 
 
 def s5_dense_gqa_attn(k_pool, v_pool, batch: Batch, q, sm_scale: float, out, lse, ws, stream=None):
     """Attention of the batch's new tokens over the whole cache (positions 0 .. t
     of each row); ``lse`` may be None.  ``ws``: ``new_workspace(batch, dense=True)``."""
     kv = _kv(k_pool, v_pool)
-    _dense_args(batch, q, out, lse, ws)
+    _dense_args(k_pool, v_pool, batch, q, out, lse, ws)
     _check(_lib.s5_dense_gqa_attn(ctypes.byref(kv), ctypes.byref(batch.desc), _ptr(q), float(sm_scale), _ptr(out),
                                   _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "s5_dense_gqa_attn")
 
@@ -394,7 +410,7 @@ def s5_dense_gqa_attn_fp8kv(k_pool, v_pool, batch: Batch, q, sm_scale: float, k_
     _need(v_pool, torch.uint8, "v_pool", tuple(k_pool.shape))
     sh = k_pool.shape
     kv = KvDesc(k_pool.data_ptr(), v_pool.data_ptr(), sh[0], sh[2], sh[1], sh[3])
-    _dense_args(batch, q, out, lse, ws)
+    _dense_args(k_pool, v_pool, batch, q, out, lse, ws)
     _check(_lib.s5_dense_gqa_attn_fp8kv(ctypes.byref(kv), ctypes.byref(batch.desc), _ptr(q), float(sm_scale),
                                         float(k_scale), float(v_scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
                                         _stream(stream)), "s5_dense_gqa_attn_fp8kv")
@@ -422,6 +438,7 @@ def s5_build_batch(req_pages, req_ids, new_lens, free_pages, batch: Batch, slots
     if pages_used is not None:
         _need(pages_used, torch.int32, "pages_used", (1,))
     _need(ws, torch.uint8, "ws")
+    _same_device(req_pages, req_ids, new_lens, free_pages, batch.page_table, slots, positions, pages_used, ws)
     reqs = RequestDesc(req_pages.data_ptr(), free_pages.data_ptr(), req_pages.shape[0], req_pages.shape[1],
                        free_pages.numel())
     _check(_lib.s5_build_batch(ctypes.byref(reqs), _ptr(req_ids), _ptr(new_lens), ctypes.byref(batch.desc),
