@@ -78,16 +78,17 @@ struct Cfg {
   static constexpr int kRowB = KV8 ? 64 : 128;
   static constexpr int kPlane = 8 * kRowB;
   static constexpr int kGroup = 3 * kPlane;
-  // Rings of about 170 KB.  Deeper ones do not stream faster but less evenly: with four V pages (bf16)
+  // Rings of 172 KB (one byte: 123 KB).  Deeper ones do not stream faster but less evenly: with four V pages (bf16)
   // the first SM ended 32 x 131,072 tokens 180 us before the last and the call took 1.89 ms, with
   // three 1.83 ms.
   static constexpr int kKStages = KV8 ? 3 : 2;                        // chunks in the K ring
-  static constexpr int kVPages = KV8 ? 6 : 3;                         // pages in the V ring
+  static constexpr int kVPages = KV8 ? 4 : 3;                         // pages in the V ring
   static constexpr int kChunkBytes = 2 * kPageBytes;
   // P: [16 groups of 8 tokens][atoms][8 tokens][kAtom bytes], swizzled over an atom's rows
   static constexpr int kPRow = kP * (KV8 ? 1 : 2);
   static constexpr int kAtom = kPRow % 128 == 0 ? 128 : 64;
   static constexpr int kPGroup = 8 * kPRow;
+  static constexpr int kPBuf = RT == 1 || (KV8 && RT == 2) ? 2 : 1;   // buffers
   // Q: [3 planes][kS rows][kRowB]
   static constexpr int kQPlane = kS * kRowB;
   // the reference sits kOff binades under the maximum it was taken from and moves when a weight
@@ -99,10 +100,10 @@ struct Cfg {
   static constexpr int kOffV = kKStages * kChunkBytes;
   static constexpr int kOffQ = kOffV + kVPages * kPageBytes;
   static constexpr int kOffP = kOffQ + 3 * kQPlane;
-  static constexpr int kOffCol = kOffP + 16 * kPGroup;                // float [6][kPairs]: per-column values
+  static constexpr int kOffCol = kOffP + kPBuf * 16 * kPGroup;                // float [6][kPairs]: per-column values
   static constexpr int kOffBad = kOffCol + 6 * kPairs * 4;            // uint32 [48]: per dim, rows that saw a non-finite value
   static constexpr int kOffBar = kOffBad + 192;
-  static constexpr int kNumBars = 2 * kKStages + 2 * kVPages + 10;
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVPages + 12;
   static constexpr int kOffMisc = kOffBar + (kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kSmem = kOffMisc + 128 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
@@ -289,6 +290,17 @@ __device__ __forceinline__ bool soft_or(bool x) {
 }
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // D[tmem] (+)= A[smem] * B[smem]^T, one K step; KV8: kind::f8f6f4, else kind::f16.
 template <bool KV8>
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, bool accumulate) {
@@ -435,8 +447,8 @@ __global__ void __launch_bounds__(kDnThreads, 1)
   uint32_t *bad_s = reinterpret_cast<uint32_t *>(smem + C::kOffBad);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
   uint64_t *k_full = bars, *k_empty = bars + KS, *v_full = bars + 2 * KS, *v_empty = v_full + VP;
-  uint64_t *s_full = v_empty + VP, *s_empty = s_full + 2, *p_full = s_full + 4, *p_free = s_full + 5;
-  uint64_t *q_full = s_full + 6, *q_empty = s_full + 7, *o_empty = s_full + 8, *b_final = s_full + 9;
+  uint64_t *s_full = v_empty + VP, *s_empty = s_full + 2, *p_full = s_full + 4, *p_free = s_full + 6;
+  uint64_t *q_full = s_full + 8, *q_empty = s_full + 9, *o_empty = s_full + 10, *b_final = s_full + 11;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
   int *abort_flag = reinterpret_cast<int *>(smem + C::kOffMisc + 4);
   int *n_bad_s = reinterpret_cast<int *>(smem + C::kOffMisc + 12);
@@ -451,9 +463,9 @@ __global__ void __launch_bounds__(kDnThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
       mbar_init(s_empty + i, 4);
+      mbar_init(p_full + i, 4);
+      mbar_init(p_free + i, 1);
     }
-    mbar_init(p_full, 4);
-    mbar_init(p_free, 1);
     mbar_init(q_full, 4);
     mbar_init(q_empty, 1);
     mbar_init(o_empty, 4);
@@ -566,15 +578,13 @@ __global__ void __launch_bounds__(kDnThreads, 1)
   Walk<RT> walk(a, start_s->q, start_s->s, start_s->off, u0, count);
   Seg x;
 
-  // Bounded wait by polling: a suspended try_wait resumes some hundred cycles after its phase
-  // completes, and three such waits are on a chunk's chain (S^T, P, the release of their buffers).
+  // Bounded wait.  (Polling with test_wait instead, without suspension, was 3% slower: the
+  // stream leaves most warps waiting, and their polls cost issue slots and power.)
   auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_test_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     while (!*reinterpret_cast<volatile int *>(abort_flag)) {
-      for (int i = 0; i < 64; ++i)
-        if (mbar_test_wait(bar, parity)) return true;
+      if (mbar_try_wait(bar, parity)) return true;
       if (globaltimer_ns() - t0 > kDnWaitNs) {
         *reinterpret_cast<volatile int *>(abort_flag) = 1;
         record_error(a.err, S5_ERR_TIMEOUT, 0);
@@ -633,77 +643,101 @@ __global__ void __launch_bounds__(kDnThreads, 1)
     }
   } else if (warp == kWarpS) {
     // ---------------- S^T = K Q^T ----------------
-    if (lane == 0) {
-      constexpr uint32_t idesc = KV8 ? tc::idesc_f8_f32(128, C::kS, 0, 0) : tc::idesc_bf16_f32(128, C::kS);
-      const uint64_t kd0 = tc::smem_desc_sw(smem_u32(sk), 16, C::kGroup, C::kRowB);
-      const uint64_t qd0 = tc::smem_desc_sw(smem_u32(sq), 16, C::kPlane, C::kRowB);
-      int gc = 0, qi = 0;
-      bool ok = true;
-      while (ok && walk.next(x)) {
-        if (!wait(q_full, qi & 1)) break;
-        for (int c = 0; c < x.np; c += 2, ++gc) {
-          const int st = gc % KS, sb = gc % C::kSBuf, use = gc / C::kSBuf;
-          if (!wait(k_full + st, (gc / KS) & 1) || (use >= 1 && !wait(s_empty + sb, (use - 1) & 1))) {
-            ok = false;
-            break;
-          }
-          tc::fence_after_sync();
+    // (The issuing warps stay converged, with counters instead of divisions and one elected lane only
+    // around the instructions, so that descriptors are built in uniform registers.)
+    constexpr uint32_t idesc = KV8 ? tc::idesc_f8_f32(128, C::kS, 0, 0) : tc::idesc_bf16_f32(128, C::kS);
+    const uint64_t kd0 = tc::smem_desc_sw(smem_u32(sk), 16, C::kGroup, C::kRowB);
+    const uint64_t qd0 = tc::smem_desc_sw(smem_u32(sq), 16, C::kPlane, C::kRowB);
+    const bool leader = elect_one();
+    int st = 0, sb = 0;                      // K stage, S^T buffer
+    uint32_t k_par = 0, s_par = 1, q_par = 0;  // (an unused buffer counts as released)
+    bool ok = true;
+    while (ok && walk.next(x)) {
+      const int np = __shfl_sync(0xffffffffu, x.np, 0);
+      ok = __all_sync(0xffffffffu, wait(q_full, q_par));
+      q_par ^= 1;
+      for (int c = 0; c < np && ok; c += 2) {
+        ok = __all_sync(0xffffffffu, wait(k_full + st, k_par) && wait(s_empty + sb, s_par));
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (leader) {
           const uint64_t kd = kd0 + (uint32_t)(st * (C::kChunkBytes >> 4));
+          const uint32_t d = tmem + sb * C::kS;
           // a K step is 32 bytes of a row: 4 (bf16) or 2 (one byte) per plane
           constexpr int kSteps = KV8 ? 6 : 12, kPer = kSteps / 3;
 #pragma unroll
           for (int kk = 0; kk < kSteps; ++kk)
-            mma_ss<KV8>(tmem + sb * C::kS, kd + (((kk / kPer) * C::kPlane + (kk % kPer) * 32) >> 4),
+            mma_ss<KV8>(d, kd + (((kk / kPer) * C::kPlane + (kk % kPer) * 32) >> 4),
                         qd0 + (((kk / kPer) * C::kQPlane + (kk % kPer) * 32) >> 4), idesc, kk > 0);
           tc::commit(k_empty + st);
           tc::commit(s_full + sb);
-          if (c + 2 >= x.np) tc::commit(q_empty);
+          if (c + 2 >= np) tc::commit(q_empty);
         }
-        ++qi;
+        __syncwarp();
+        if (++st == KS) {
+          st = 0;
+          k_par ^= 1;
+        }
+        if (++sb == C::kSBuf) {
+          sb = 0;
+          s_par ^= 1;
+        }
       }
-      tc::commit(b_final);  // arrives once every MMA issued above has completed
     }
+    if (leader) tc::commit(b_final);  // arrives once every MMA issued above has completed
   } else if (warp == kWarpPv) {
     // ---------------- O^T += V^T P^T ----------------
-    if (lane == 0) {
-      constexpr uint32_t base = (KV8 ? tc::idesc_f8_f32(0, C::kP, 0, 1) : tc::idesc_bf16_f32(0, C::kP)) | tc::kIdescMnA |
-                                tc::kIdescMnB;
-      constexpr uint32_t id1 = base | (128u >> 4) << 24, id2 = base | (64u >> 4) << 24;
-      const uint64_t vd0 = tc::smem_desc_sw(smem_u32(sv), C::kPlane, C::kGroup, C::kRowB);
-      const uint64_t pd0 = tc::smem_desc_sw(smem_u32(sp), 8 * C::kAtom, C::kPGroup, C::kAtom);
-      int gc = 0, vp = 0, qi = 0;  // chunks, V pages, runs so far
-      bool ok = true;
-      while (ok && walk.next(x)) {
-        for (int c = 0; c < x.np && ok; c += 2, ++gc) {
-          if (!wait(p_full, gc & 1) || (c == 0 && qi > 0 && !wait(o_empty, (qi - 1) & 1))) {
-            ok = false;
-            break;
-          }
-          const int m = min(2, x.np - c);  // (a run's last page may stand alone)
-          for (int y = 0; y < m; ++y, ++vp) {
-            const int st = vp % VP;
-            if (!wait(v_full + st, (vp / VP) & 1)) {
-              ok = false;
-              break;
-            }
-            tc::fence_after_sync();
-            constexpr int kSteps = KV8 ? 2 : 4, kGrp = 8 / kSteps;  // K steps of a page, 8-token groups of a step
-            const uint64_t vd = vd0 + (uint32_t)(st * (PB >> 4));
-            const uint64_t pd = pd0 + (uint32_t)(y * (8 * C::kPGroup >> 4));
+    constexpr uint32_t base = (KV8 ? tc::idesc_f8_f32(0, C::kP, 0, 1) : tc::idesc_bf16_f32(0, C::kP)) | tc::kIdescMnA |
+                              tc::kIdescMnB;
+    constexpr uint32_t id1 = base | (128u >> 4) << 24, id2 = base | (64u >> 4) << 24;
+    const uint64_t vd0 = tc::smem_desc_sw(smem_u32(sv), C::kPlane, C::kGroup, C::kRowB);
+    const uint64_t pd0 = tc::smem_desc_sw(smem_u32(sp), 8 * C::kAtom, C::kPGroup, C::kAtom);
+    const bool leader = elect_one();
+    int st = 0, pb = 0;                       // V page, P buffer
+    uint32_t v_par = 0, p_par = 0, o_par = 1;
+    bool ok = true;
+    auto page = [&](int y, bool first) {  // page y of the chunk
+      if (leader) {
+        constexpr int kSteps = KV8 ? 2 : 4, kGrp = 8 / kSteps;  // K steps of a page, 8-token groups of a step
+        const uint64_t vd = vd0 + (uint32_t)(st * (PB >> 4));
+        const uint64_t pd = pd0 + (uint32_t)((2 * pb + y) * (8 * C::kPGroup >> 4));
 #pragma unroll
-            for (int ks = 0; ks < kSteps; ++ks) {
-              const uint64_t vk = vd + (ks * kGrp * C::kGroup >> 4), pk = pd + (ks * kGrp * C::kPGroup >> 4);
-              mma_ss<KV8>(tmem + C::kTmO, vk, pk, id1, c + y + ks > 0);
-              mma_ss<KV8>(tmem + C::kTmO2, vk + (2 * C::kPlane >> 4), pk, id2, c + y + ks > 0);
-            }
-            tc::commit(v_empty + st);
-          }
-          if (ok) tc::commit(p_free);
+        for (int ks = 0; ks < kSteps; ++ks) {
+          const uint64_t vk = vd + (ks * kGrp * C::kGroup >> 4), pk = pd + (ks * kGrp * C::kPGroup >> 4);
+          mma_ss<KV8>(tmem + C::kTmO, vk, pk, id1, !first || ks > 0);
+          mma_ss<KV8>(tmem + C::kTmO2, vk + (2 * C::kPlane >> 4), pk, id2, !first || ks > 0);
         }
-        ++qi;
+        tc::commit(v_empty + st);
       }
-      tc::commit(b_final);
+      __syncwarp();
+      if (++st == VP) {
+        st = 0;
+        v_par ^= 1;
+      }
+    };
+    while (ok && walk.next(x)) {
+      const int np = __shfl_sync(0xffffffffu, x.np, 0);
+      for (int c = 0; c < np; c += 2) {
+        // V first: it is there long before P (unless the stream is behind)
+        ok = __all_sync(0xffffffffu, wait(v_full + st, v_par) && wait(p_full + pb, p_par) && (c > 0 || wait(o_empty, o_par)));
+        if (!ok) break;
+        tc::fence_after_sync();
+        page(0, c == 0);
+        if (c + 1 < np) {  // (a run's last page may stand alone)
+          ok = __all_sync(0xffffffffu, wait(v_full + st, v_par));
+          if (!ok) break;
+          page(1, false);
+        }
+        if (leader) tc::commit(p_free + pb);
+        __syncwarp();
+        if (++pb == C::kPBuf) {
+          pb = 0;
+          p_par ^= 1;
+        }
+      }
+      o_par ^= 1;
     }
+    if (leader) tc::commit(b_final);
   } else {
     // ---------------- softmax and epilogue: thread tid is token tid of the chunk, then dim tid ----------------
     const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
@@ -734,15 +768,14 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       for (int i = 0; i < NQ / 2; ++i) l[i] = make_float2(0.f, 0.f);
       bool force = true;  // some column has no reference yet
       const int32_t *pt = a.page_table + (size_t)x.s * a.max_pages + x.p0;
-      int ids = -1, nxt = lane < x.np ? ld_cg(pt + lane) : -1;
+      int nxt = lane < x.np ? ld_cg(pt + lane) : -1;
+      uint32_t good = 0;  // bit i: page i of the current 32 is in the pool (none behind the run's last)
       for (int c = 0; c < x.np; c += 2, ++gc) {
         if ((c & 31) == 0) {
-          ids = nxt;
+          good = __ballot_sync(0xffffffffu, nxt >= 0 && nxt < a.num_pages);
           nxt = c + 32 + lane < x.np ? ld_cg(pt + c + 32 + lane) : -1;
         }
-        // (a page behind the run's last reads as -1: no token of it is visible)
-        const int pa = __shfl_sync(0xffffffffu, ids, c & 31), pb = __shfl_sync(0xffffffffu, ids, (c & 31) + 1);
-        const bool ok_a = pa >= 0 && pa < a.num_pages, ok_b = pb >= 0 && pb < a.num_pages;
+        const bool ok_a = (good >> (c & 31)) & 1, ok_b = (good >> (c & 31)) & 2;
         const int base = (x.p0 + c) * kPage;
         const bool masked = !ok_a || !ok_b || base + kChunk - 1 > x.t0;
         const int sb = gc % C::kSBuf;
@@ -829,7 +862,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
             l[i].y *= co.y;
           }
           if (c > 0) {  // O^T holds the chunks before: after their last product
-            ok = wait(p_free, (gc - 1) & 1) && ok;
+            ok = wait(p_free + (gc - 1) % C::kPBuf, ((gc - 1) / C::kPBuf) & 1) && ok;
             __syncwarp();
             tc::fence_after_sync();
 #pragma unroll 1
@@ -845,10 +878,11 @@ __global__ void __launch_bounds__(kDnThreads, 1)
             tc::wait_st();
           }
         }
-        // P, last read by the products of the chunk before
-        if (gc >= 1) ok = wait(p_free, (gc - 1) & 1) && ok;
+        // P, last read by the products of the chunk kPBuf before
+        const int pbuf = gc % C::kPBuf;
+        if (gc >= C::kPBuf) ok = wait(p_free + pbuf, (gc / C::kPBuf - 1) & 1) && ok;
         {
-          uint8_t *row = sp + (tid >> 3) * C::kPGroup + (tid & 7) * C::kAtom;
+          uint8_t *row = sp + pbuf * 16 * C::kPGroup + (tid >> 3) * C::kPGroup + (tid & 7) * C::kAtom;
           const int sw = C::kAtom == 128 ? tid & 7 : (tid >> 1) & 3;
           constexpr int kPer = C::kAtom / 16;  // 16-byte pieces of an atom's row
           auto piece = [&](int i) {
@@ -895,7 +929,10 @@ __global__ void __launch_bounds__(kDnThreads, 1)
           }
         }
         if (masked) {
-          // V of tokens that a row of the tile does not see must not be NaN or infinite
+          // V of tokens that a row of the tile does not see must not be NaN or infinite.  (The chunk before
+          // must be done: until its pages have been consumed, a wait for this chunk's pages could take
+          // the ring slot's phase before last for the one it waits for.)
+          if (gc >= 1) ok = wait(p_free + (gc - 1) % C::kPBuf, ((gc - 1) / C::kPBuf) & 1) && ok;
 #pragma unroll 1
           for (int y = 0; y < min(2, x.np - c); ++y) {
             const int st = (vp + y) % VP, first = base + y * kPage;
@@ -909,7 +946,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         fence_proxy_async_smem();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
+        if (lane == 0) mbar_arrive(p_full + pbuf);
       }
 
       // ---- the run's result ----
@@ -941,10 +978,11 @@ __global__ void __launch_bounds__(kDnThreads, 1)
             v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
           }
         }
+        // the last products: once they are done, no warp reads what a moved reference left in warp_s
+        ok = wait(p_free + (gc - 1) % C::kPBuf, ((gc - 1) / C::kPBuf) & 1) && ok;
         warp_s[warp * NQ + at] = v[0];
         if constexpr (NQ == 64) warp_s[warp * NQ + at + 1] = v[1];
       }
-      ok = wait(p_free, (gc - 1) & 1) && ok;
       if (soft_or(!ok)) {
         ok = false;
         break;

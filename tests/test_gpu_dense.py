@@ -180,6 +180,22 @@ def test_without_lse_and_repeatable(lib, kv):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("hi,nq", [(300, 1), (4000, 1), (2500, 4)])
+def test_ragged_batches_repeat_bit_for_bit(lib, kv, hi, nq):
+    """Many sequences per CTA, runs of one chunk among them: right, and the same every time."""
+    g = torch.Generator().manual_seed(hi)
+    n = 150
+    ctx = torch.randint(0, hi, (n,), generator=g).tolist()
+    new = torch.randint(1, nq + 1, (n,), generator=g).tolist()
+    c = Case(ctx, new, kv, seed=hi + nq, k_scale=1 / 64, v_scale=1 / 64).run(lib).check()
+    out, lse = c.out.clone(), c.lse.clone()
+    for _ in range(100):
+        c.out.fill_(9.0)
+        c.call(lib)
+        assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_rows_behind_the_batch_stay(lib, kv):
     c = Case([500, 3], [2, 1], kv, seed=4, pad_rows=6, k_scale=1 / 64, v_scale=1 / 64).run(lib).check()
     assert bool((c.out[3:] == 7.0).all()) and bool((c.lse[3:] == 7.0).all())
