@@ -27,6 +27,7 @@ namespace {
 constexpr int kBThreads = 256;
 constexpr int kBPer = 4;                       // sequences per thread and round
 constexpr int kBSeqs = kBThreads * kBPer;      // sequences per round
+constexpr int kBCols = 256;                    // table columns per warp and step
 constexpr int kBMaxBatch = 65535;              // page sums stay below 2^31 (32,768 pages per sequence)
 
 struct BuildArgs {
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(kBThreads) build_batch_kernel(const BuildArgs 
   __shared__ long long rbuf[kBThreads / 32];
   __shared__ int tot_pages;
   __shared__ long long tot_rows;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   int pages0 = 0;       // sums over the rounds before
   long long rows0 = 0;
@@ -131,46 +132,46 @@ __global__ void __launch_bounds__(kBThreads) build_batch_kernel(const BuildArgs 
     if (tid == 0) s_cu[kBSeqs] = (int)min(rows0, (long long)a.total_q);
     __syncthreads();
 
-    // ---- table entries ----
-    constexpr int W = VEC ? 4 : 1;
-    const int per_row = a.max_pages / W;
-    const int units = n * per_row;  // <= 1,024 * 2^15 (the host bounds max_pages)
-    const int step = gridDim.x * kBThreads;
-    for (int u = blockIdx.x * kBThreads + tid; u < units; u += step) {
-      const int k = u / per_row, c = (u - k * per_row) * W;
-      const int h = s_held[k], nd = s_need[k];
-      int32_t v[W];
-      int32_t *req = a.req_pages + (size_t)max(s_id[k], 0) * a.req_stride + c;
-      if (VEC && c < h) {
-        const int4 x = *reinterpret_cast<const int4 *>(req);
-        v[0] = x.x;
-        v[W > 1 ? 1 : 0] = x.y;
-        v[W > 2 ? 2 : 0] = x.z;
-        v[W > 3 ? 3 : 0] = x.w;
-      }
+    // ---- table entries: a warp takes 256 columns of a row, their loads in flight together ----
+    const int segs = (a.max_pages + kBCols - 1) / kBCols;
+    const int units = n * segs;  // <= 1,024 * 2^12 (the host bounds max_pages)
+    for (int u = blockIdx.x * (kBThreads / 32) + warp; u < units; u += gridDim.x * (kBThreads / 32)) {
+      const int k = u / segs, c0 = (u - k * segs) * kBCols;
+      const int h = s_held[k], nd = s_need[k], take = s_take[k] - h;
+      int32_t *req = a.req_pages + (size_t)max(s_id[k], 0) * a.req_stride;
+      int32_t *dst = a.page_table + (size_t)(s0 + k) * a.max_pages;
+      constexpr int W = VEC ? 4 : 1, N = kBCols / (32 * W);  // columns of a piece, pieces of a lane
+      int32_t v[N][W];
 #pragma unroll
-      for (int e = 0; e < W; ++e) {
-        if (c + e >= h) {
-          v[e] = -1;
-          if (c + e < nd) {
-            const int f = s_take[k] + c + e - h;
-            if (f < a.num_free) v[e] = ld_cg(a.free_pages + f);
-            req[e] = v[e];
-          }
-        } else if (!VEC) {
-          v[e] = req[e];
+      for (int i = 0; i < N; ++i) {
+        const int c = c0 + (i * 32 + lane) * W;
+        if (VEC) {
+          if (c < h) *reinterpret_cast<int4 *>(v[i]) = *reinterpret_cast<const int4 *>(req + c);
+        } else if (c < h) {
+          v[i][0] = req[c];
         }
       }
-      int32_t *dst = a.page_table + (size_t)(s0 + k) * a.max_pages + c;
-      if (VEC)
-        *reinterpret_cast<int4 *>(dst) = make_int4(v[0], v[W > 1 ? 1 : 0], v[W > 2 ? 2 : 0], v[W > 3 ? 3 : 0]);
-      else
-        dst[0] = v[0];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = c0 + (i * 32 + lane) * W;
+        if (c >= a.max_pages) continue;
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          if (c + e < h) continue;
+          v[i][e] = -1;
+          if (c + e < nd) {  // a page taken now
+            if (take + c + e < a.num_free) v[i][e] = ld_cg(a.free_pages + take + c + e);
+            req[c + e] = v[i][e];
+          }
+        }
+        if (VEC) *reinterpret_cast<int4 *>(dst + c) = *reinterpret_cast<const int4 *>(v[i]);
+        else dst[c] = v[i][0];
+      }
     }
     // ---- rows ----
     if (a.slots != nullptr || a.positions != nullptr) {
-      for (int r = s_cu[0] + blockIdx.x * kBThreads + tid; r < s_cu[kBSeqs]; r += step) {
-        int lo = 0, hi = kBSeqs;  // the last k with s_cu[k] <= r: the sequence that has row r
+      for (int r = s_cu[0] + blockIdx.x * kBThreads + tid; r < s_cu[kBSeqs]; r += gridDim.x * kBThreads) {
+        int lo = 0, hi = n;  // the last k with s_cu[k] <= r: the sequence that has row r
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
           if (s_cu[mid] <= r) lo = mid;
@@ -244,9 +245,10 @@ extern "C" s5_status s5_build_batch(const s5_request_desc *requests, const int32
   const bool vec = batch->max_pages % 4 == 0 && requests->req_stride % 4 == 0 && aligned16(batch->page_table) &&
                    aligned16(requests->req_pages);
   const int rounds_seqs = batch->batch < kBSeqs ? batch->batch : kBSeqs;
-  long long work = (long long)rounds_seqs * batch->max_pages / (vec ? 4 : 1);
-  if (batch->total_q > work) work = batch->total_q;
-  long long grid = (work + kBThreads - 1) / kBThreads;
+  constexpr int kWarps = kBThreads / 32;
+  const long long by_table = ((long long)rounds_seqs * ((batch->max_pages + kBCols - 1) / kBCols) + kWarps - 1) / kWarps;
+  const long long by_rows = ((long long)batch->total_q + kBThreads - 1) / kBThreads;
+  long long grid = by_table > by_rows ? by_table : by_rows;
   if (grid > 148 * 4) grid = 148 * 4;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);

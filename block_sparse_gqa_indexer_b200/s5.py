@@ -130,7 +130,7 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -378,7 +378,7 @@ def s5_append_kv_fp8(k_pool, v_pool, key_pool, batch: Batch, k_new, v_new, key_n
 
 def _same_device(*tensors):
     """The kernels run on the current device: every tensor has to be there."""
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{dev}")
@@ -424,19 +424,14 @@ def s5_build_batch(req_pages, req_ids, new_lens, free_pages, batch: Batch, slots
     [num_reqs][stride] (which receives the pages taken from ``free_pages``), the
     request of each sequence ``req_ids`` [batch] (-1: empty), ``batch.ctx_lens``
     and ``new_lens`` [batch].  ``batch.total_q`` is the sum of the new tokens."""
-    _need(req_pages, torch.int32, "req_pages")
+    n, rows = batch.ctx_lens.shape, (batch.total_q,)
+    for name, t, shape in (("req_pages", req_pages, None), ("req_ids", req_ids, n), ("new_lens", new_lens, n),
+                           ("free_pages", free_pages, None), ("slots", slots, rows), ("positions", positions, rows),
+                           ("pages_used", pages_used, (1,))):
+        if t is not None or name in ("req_pages", "req_ids", "new_lens", "free_pages"):
+            _need(t, torch.int32, name, shape)
     if req_pages.dim() != 2:
         raise ValueError("req_pages must be [num_reqs][stride]")
-    n = batch.ctx_lens.numel()
-    _need(req_ids, torch.int32, "req_ids", (n,))
-    _need(new_lens, torch.int32, "new_lens", (n,))
-    _need(free_pages, torch.int32, "free_pages", (free_pages.numel(),))
-    if slots is not None:
-        _need(slots, torch.int32, "slots", (batch.total_q,))
-    if positions is not None:
-        _need(positions, torch.int32, "positions", (batch.total_q,))
-    if pages_used is not None:
-        _need(pages_used, torch.int32, "pages_used", (1,))
     _need(ws, torch.uint8, "ws")
     _same_device(req_pages, req_ids, new_lens, free_pages, batch.page_table, slots, positions, pages_used, ws)
     reqs = RequestDesc(req_pages.data_ptr(), free_pages.data_ptr(), req_pages.shape[0], req_pages.shape[1],
