@@ -96,6 +96,9 @@ struct Cfg {
   // weights of 2^-28 of the largest still count.
   static constexpr float kOff = KV8 ? 12.f : 0.f;
   static constexpr float kTop = KV8 ? 15.f : 8.f;
+  // What a run costs besides its pages, in pages, for equal shares: 64 ragged requests' SMs took 2 us a
+  // run, 16 verified requests' (4 rows) 7 us.
+  static constexpr int kStart = (RT == 1 ? 2 : RT == 2 ? 4 : 6) * (KV8 ? 2 : 1);
   // shared memory (from a 1,024-byte aligned base)
   static constexpr int kOffV = kKStages * kChunkBytes;
   static constexpr int kOffQ = kOffV + kVPages * kPageBytes;
@@ -146,12 +149,19 @@ __device__ __forceinline__ Seq load_seq(const DenseArgs &a, int s) {
   return q;
 }
 
-template <int RT>
-__device__ __forceinline__ long long group_pages(const Seq &q) {  // of one KV group of the sequence
+// Units of the first m tiles, full ones: a tile counts its pages and, before them, START units for
+// what beginning and ending a run costs.
+template <int RT, int START>
+__device__ __forceinline__ long long full_tile_units(int ctx, int m) {
+  return full_tile_pages<RT>(ctx, m) + (long long)START * m;
+}
+
+template <int RT, int START>
+__device__ __forceinline__ long long group_units(const Seq &q) {  // of one KV group of the sequence
   if (q.n <= 0) return 0;
   const int tiles = (q.n + RT - 1) / RT;
-  const long long last = (q.ctx + q.n + kPage - 1) / kPage;
-  return tiles == 1 ? last : full_tile_pages<RT>(q.ctx, tiles - 1) + last;
+  const long long last = (q.ctx + q.n + kPage - 1) / kPage + START;
+  return tiles == 1 ? last : full_tile_units<RT, START>(q.ctx, tiles - 1) + last;
 }
 
 // Where a CTA's share begins: unit `off` of sequence s.
@@ -165,37 +175,45 @@ struct Start {
 struct Seg {
   int s, g, row0, nr, t0;    // sequence, KV group, first row, rows, position of the first row
   int p0, np, tile_pages;    // first page, pages, pages of the whole tile
-  long long tile_u;          // unit of the tile's first page
+  long long tile_u;          // unit of the tile's first page (after its START units)
 };
 
 // The runs of one CTA in order.  Every warp walks them by itself.
-template <int RT>
+template <int RT, int START>
 struct Walk {
   const DenseArgs &a;
   Seq q;
-  int s, g, k, p;
+  int s, g, k, o;  // sequence, group, tile, unit of the tile that comes next
   long long u, rem;
 
   // unit u0 is unit `off` of sequence s0
   __device__ Walk(const DenseArgs &args, const Seq &q0, int s0, long long off, long long u0, long long count)
       : a(args), q(q0), s(s0), g(0), u(u0), rem(count) {
-    const long long per = group_pages<RT>(q);
-    long long o = off;
-    while (o >= per) {
-      o -= per;
+    const long long per = group_units<RT, START>(q);
+    long long left = off;
+    while (left >= per) {
+      left -= per;
       ++g;
     }
-    int lo = 0, hi = (q.n + RT - 1) / RT;  // the last tile k whose pages before are <= o
+    int lo = 0, hi = (q.n + RT - 1) / RT;  // the last tile k whose units before are <= left
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (full_tile_pages<RT>(q.ctx, mid) <= o) lo = mid;
+      if (full_tile_units<RT, START>(q.ctx, mid) <= left) lo = mid;
       else hi = mid;
     }
     k = lo;
-    p = (int)(o - full_tile_pages<RT>(q.ctx, k));
+    o = (int)(left - full_tile_units<RT, START>(q.ctx, k));
+    skip_start();
   }
 
-  __device__ void run(Seg &x) const {  // the run that starts here
+  __device__ void skip_start() {
+    const int n = (int)min((long long)max(START - o, 0), rem);
+    o += n;
+    u += n;
+    rem -= n;
+  }
+
+  __device__ void run(Seg &x) const {  // the run that starts here (rem > 0)
     const int nr = min(RT, q.n - k * RT);
     x.s = s;
     x.g = g;
@@ -203,9 +221,9 @@ struct Walk {
     x.nr = nr;
     x.t0 = q.ctx + k * RT;
     x.tile_pages = (x.t0 + nr + kPage - 1) / kPage;
-    x.p0 = p;
-    x.np = (int)min((long long)(x.tile_pages - p), rem);
-    x.tile_u = u - p;
+    x.p0 = o - START;
+    x.np = (int)min((long long)(x.tile_pages - x.p0), rem);
+    x.tile_u = u - x.p0;
   }
 
   __device__ bool next(Seg &x) {
@@ -213,9 +231,9 @@ struct Walk {
     run(x);
     u += x.np;
     rem -= x.np;
-    p += x.np;
-    if (p == x.tile_pages) {
-      p = 0;
+    o += x.np;
+    if (o == x.tile_pages + START) {
+      o = 0;
       if (++k * RT >= q.n) {
         k = 0;
         if (++g == kKv) {
@@ -225,6 +243,7 @@ struct Walk {
           if (q.n == 0) rem = 0;
         }
       }
+      skip_start();
     }
     return true;
   }
@@ -480,8 +499,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
 
   if (tid == kWarpK * 32) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
   if (tid == kWarpV * 32) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
-  pdl_wait();     // (programmatic launch) global memory is read from here on
-  pdl_trigger();  // the joining kernel's CTAs may take the SMs as they become free, and wait there
+  pdl_wait();  // (programmatic launch) global memory is read from here on
   if (tid == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
 
   // ---- this CTA's share: prefix sums of the sequences' page units ----
@@ -502,7 +520,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
 #pragma unroll
     for (int i = 0; i < kScanPer; ++i) {
       const int s = (r * kDnThreads + tid) * per + i;
-      units[i] = kKv * group_pages<RT>(seqs[i]);
+        units[i] = kKv * group_units<RT, C::kStart>(seqs[i]);
       mine += units[i];
       if (seqs[i].bad && report && s % (int)gridDim.x == (int)blockIdx.x) {
         record_error(a.err, S5_ERR_DEVICE_BOUNDS, max(seqs[i].lo, 0));
@@ -575,7 +593,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
     if (warp == kWarpPv) tc::tmem_dealloc(tmem, C::kTmCols);
     return;
   }
-  Walk<RT> walk(a, start_s->q, start_s->s, start_s->off, u0, count);
+  Walk<RT, C::kStart> walk(a, start_s->q, start_s->s, start_s->off, u0, count);
   Seg x;
 
   // Bounded wait.  (Polling with test_wait instead, without suspension, was 3% slower: the
@@ -753,8 +771,10 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
     };
-    walk.run(x);
-    stage_q(x);
+    if (walk.rem > 0) {
+      walk.run(x);
+      stage_q(x);
+    }
     while (walk.next(x)) {
       const int t_last = x.t0 + x.nr - 1;
       if (tid < NQ) ref_s[tid] = 0.f;
