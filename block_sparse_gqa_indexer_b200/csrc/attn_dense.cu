@@ -106,7 +106,7 @@ struct Cfg {
   static constexpr int kOffCol = kOffP + kPBuf * 16 * kPGroup;                // float [6][kPairs]: per-column values
   static constexpr int kOffBad = kOffCol + 6 * kPairs * 4;            // uint32 [48]: per dim, rows that saw a non-finite value
   static constexpr int kOffBar = kOffBad + 192;
-  static constexpr int kNumBars = 2 * kKStages + 2 * kVPages + 12;
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVPages + 13;
   static constexpr int kOffMisc = kOffBar + (kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kSmem = kOffMisc + 128 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
@@ -468,6 +468,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
   uint64_t *k_full = bars, *k_empty = bars + KS, *v_full = bars + 2 * KS, *v_empty = v_full + VP;
   uint64_t *s_full = v_empty + VP, *s_empty = s_full + 2, *p_full = s_full + 4, *p_free = s_full + 6;
   uint64_t *q_full = s_full + 8, *q_empty = s_full + 9, *o_empty = s_full + 10, *b_final = s_full + 11;
+  uint64_t *b_stall = s_full + 12;  // nothing ever arrives on it (expired-wait test hook)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
   int *abort_flag = reinterpret_cast<int *>(smem + C::kOffMisc + 4);
   int *n_bad_s = reinterpret_cast<int *>(smem + C::kOffMisc + 12);
@@ -489,6 +490,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
     mbar_init(q_empty, 1);
     mbar_init(o_empty, 4);
     mbar_init(b_final, 2);
+    mbar_init(b_stall, 1);
     *abort_flag = 0;
     *n_bad_s = 0;
   }
@@ -598,12 +600,12 @@ __global__ void __launch_bounds__(kDnThreads, 1)
 
   // Bounded wait.  (Polling with test_wait instead, without suspension, was 3% slower: the
   // stream leaves most warps waiting, and their polls cost issue slots and power.)
-  auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+  auto wait = [&](uint64_t *bar, uint32_t parity, uint64_t limit_ns = kDnWaitNs) -> bool {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     while (!*reinterpret_cast<volatile int *>(abort_flag)) {
       if (mbar_try_wait(bar, parity)) return true;
-      if (globaltimer_ns() - t0 > kDnWaitNs) {
+      if (globaltimer_ns() - t0 > limit_ns) {
         *reinterpret_cast<volatile int *>(abort_flag) = 1;
         record_error(a.err, S5_ERR_TIMEOUT, 0);
       }
@@ -667,7 +669,9 @@ __global__ void __launch_bounds__(kDnThreads, 1)
     const uint64_t kd0 = tc::smem_desc_sw(smem_u32(sk), 16, C::kGroup, C::kRowB);
     const uint64_t qd0 = tc::smem_desc_sw(smem_u32(sq), 16, C::kPlane, C::kRowB);
     const bool leader = elect_one();
-    int st = 0, sb = 0;                      // K stage, S^T buffer
+    // test hook (workspace header, zero in normal use): wait that many ns for nothing, then give up
+    uint64_t stall_ns = a.err != nullptr ? ld_cg_u64(reinterpret_cast<const uint64_t *>(a.err) + kWsStallWord) : 0;
+    int st = 0, sb = 0;                        // K stage, S^T buffer
     uint32_t k_par = 0, s_par = 1, q_par = 0;  // (an unused buffer counts as released)
     bool ok = true;
     while (ok && walk.next(x)) {
@@ -676,6 +680,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       q_par ^= 1;
       for (int c = 0; c < np && ok; c += 2) {
         ok = __all_sync(0xffffffffu, wait(k_full + st, k_par) && wait(s_empty + sb, s_par));
+        if (ok && stall_ns != 0) ok = __all_sync(0xffffffffu, wait(b_stall, 0, stall_ns));
         if (!ok) break;
         tc::fence_after_sync();
         if (leader) {
@@ -799,7 +804,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         const int base = (x.p0 + c) * kPage;
         const bool masked = !ok_a || !ok_b || base + kChunk - 1 > x.t0;
         const int sb = gc % C::kSBuf;
-        ok = wait(s_full + sb, (gc / C::kSBuf) & 1) && ok;
+        ok = ok && wait(s_full + sb, (gc / C::kSBuf) & 1);
         __syncwarp();
         tc::fence_after_sync();
         // the token's scores, two columns per element
@@ -882,7 +887,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
             l[i].y *= co.y;
           }
           if (c > 0) {  // O^T holds the chunks before: after their last product
-            ok = wait(p_free + (gc - 1) % C::kPBuf, ((gc - 1) / C::kPBuf) & 1) && ok;
+            ok = ok && wait(p_free + (gc - 1) % C::kPBuf, ((gc - 1) / C::kPBuf) & 1);
             __syncwarp();
             tc::fence_after_sync();
 #pragma unroll 1
@@ -900,7 +905,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         }
         // P, last read by the products of the chunk kPBuf before
         const int pbuf = gc % C::kPBuf;
-        if (gc >= C::kPBuf) ok = wait(p_free + pbuf, (gc / C::kPBuf - 1) & 1) && ok;
+        if (gc >= C::kPBuf) ok = ok && wait(p_free + pbuf, (gc / C::kPBuf - 1) & 1);
         {
           uint8_t *row = sp + pbuf * 16 * C::kPGroup + (tid >> 3) * C::kPGroup + (tid & 7) * C::kAtom;
           const int sw = C::kAtom == 128 ? tid & 7 : (tid >> 1) & 3;
@@ -952,13 +957,13 @@ __global__ void __launch_bounds__(kDnThreads, 1)
           // V of tokens that a row of the tile does not see must not be NaN or infinite.  (The chunk before
           // must be done: until its pages have been consumed, a wait for this chunk's pages could take
           // the ring slot's phase before last for the one it waits for.)
-          if (gc >= 1) ok = wait(p_free + (gc - 1) % C::kPBuf, ((gc - 1) / C::kPBuf) & 1) && ok;
+          if (gc >= 1) ok = ok && wait(p_free + (gc - 1) % C::kPBuf, ((gc - 1) / C::kPBuf) & 1);
 #pragma unroll 1
           for (int y = 0; y < min(2, x.np - c); ++y) {
             const int st = (vp + y) % VP, first = base + y * kPage;
             const bool ok_y = y == 0 ? ok_a : ok_b;
             if (ok_y && first + kPage - 1 <= x.t0) continue;
-            ok = wait(v_full + st, ((vp + y) / VP) & 1) && ok;
+            ok = ok && wait(v_full + st, ((vp + y) / VP) & 1);
             clean_v<KV8, RT>(sv + st * PB, bad_s, ok_y, x.t0 - first, t_last - first, tid);
           }
         }
@@ -971,7 +976,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
 
       // ---- the run's result ----
       if (walk.rem > 0) {  // the next run's Q first, so that its first scores are there after this epilogue
-        ok = wait(q_empty, qi & 1) && ok;
+        ok = ok && wait(q_empty, qi & 1);
         Seg y;
         walk.run(y);
         stage_q(y);
@@ -999,7 +1004,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
           }
         }
         // the last products: once they are done, no warp reads what a moved reference left in warp_s
-        ok = wait(p_free + (gc - 1) % C::kPBuf, ((gc - 1) / C::kPBuf) & 1) && ok;
+        ok = ok && wait(p_free + (gc - 1) % C::kPBuf, ((gc - 1) / C::kPBuf) & 1);
         warp_s[warp * NQ + at] = v[0];
         if constexpr (NQ == 64) warp_s[warp * NQ + at + 1] = v[1];
       }

@@ -136,7 +136,8 @@ typedef struct {
  * wait that long, after its first block copies land, on a barrier that nothing
  * arrives on, and then take the expired-wait path: it records S5_ERR_TIMEOUT,
  * waits (bounded) for its copies still in flight and returns with zero output
- * for its unit.  Zeroing the workspace or s5_reset_device_error clears it. */
+ * for its unit.  The dense attention kernel does the same after its first K
+ * pages land (the rows of that call are then undefined).  Zeroing the workspace or s5_reset_device_error clears it. */
 #define S5_WS_TEST_STALL_OFFSET 64
 s5_status s5_workspace_size(const s5_batch_desc *batch, int32_t window, size_t *bytes);
 
@@ -319,8 +320,9 @@ s5_status s5_append_kv_fp8(const s5_kv_desc *kv, const s5_index_desc *index, con
  * For row r at position t and head h (group g = h / 16):
  *   out = sum_{j <= t} softmax_j(sm_scale * q[r][h] . K[j][g]) V[j][g]
  *   lse = log sum_{j <= t} exp(sm_scale * q[r][h] . K[j][g])   (may be NULL)
- * A sequence's cache is split over as many CTAs as balance the batch (from the
- * device's lengths, so ragged batches balance too) and the parts are joined by
+ * A sequence's cache is split over the SMs in equal shares (from the device's
+ * lengths, so ragged batches balance too; the shares and with them the results
+ * depend on the lengths and the GPU's SM count only) and the parts are joined by
  * their log-sum-exp.  K or V values at positions > t never reach row r, not
  * even as infinities or NaN.  A V value at a position <= t that is not finite
  * makes its dimension of the row's 16 heads not finite (NaN or an infinity); a
@@ -334,6 +336,8 @@ s5_status s5_append_kv_fp8(const s5_kv_desc *kv, const s5_index_desc *index, con
  *     above max_len gives zeros and lse = -inf in its rows (info = its first
  *     row); the tokens of a page id outside the pool take no part (info = a
  *     row that would read it).  Other rows are unaffected.
+ *   max_q: sequences of up to max_q <= 4 new tokens read their cache once for
+ *     all of them; with more, once per 4 tokens.
  *   limits: total_q * 64 <= 2^31 - 1, num_pages * 256 < 2^31
  *     (S5_ERR_UNSUPPORTED otherwise).
  * The workspace is the one of s5_workspace_size_dense (which also covers every
@@ -344,8 +348,12 @@ s5_status s5_dense_gqa_attn(const s5_kv_desc *kv, const s5_batch_desc *batch, co
                             float *lse, void *workspace, size_t workspace_bytes, s5_stream_t stream);
 
 /* s5_dense_gqa_attn over one-byte KV: pools, codes and scales as in
- * s5_sparse_gqa_attn_fp8kv.  k_scale, v_scale and sm_scale * k_scale must be
- * finite (S5_ERR_INVALID_ARG). */
+ * s5_sparse_gqa_attn_fp8kv.  Products run on 8-bit tensor cores with the other
+ * operand in terms: q as two E4M3 values of q times a power of two (exact for
+ * bf16 values down to 2^-14 of the row and head's largest magnitude, smaller ones
+ * to 2^-21 of it); a weight in f16 as E5M2 values, together exact (max_q <= 2) or
+ * within 2^-9 of the weight, and to 2^-28 of the largest.  k_scale, v_scale and
+ * sm_scale * k_scale must be finite (S5_ERR_INVALID_ARG). */
 s5_status s5_dense_gqa_attn_fp8kv(const s5_kv_desc *kv, const s5_batch_desc *batch, const void *q, float sm_scale,
                                   float k_scale, float v_scale, void *out, float *lse, void *workspace,
                                   size_t workspace_bytes, s5_stream_t stream);

@@ -394,6 +394,36 @@ def test_other_stream_and_shared_workspace(lib):
     assert lib.s5_get_device_error(ws)[0] == 0
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("max_q", [1, 2, 3, 50])
+def test_max_q_need_not_be_tight(lib, kv, max_q):
+    """max_q chooses the rows of a tile; any value gives every row its answer."""
+    c = Case([300, 64, 0, 900], [5, 1, 3, 2], kv, seed=19, k_scale=1 / 64, v_scale=1 / 64).make(lib)
+    c.batch = lib.Batch(c.table, c.batch.ctx_lens, c.batch.cu_q, c.total_q, max_q, c.max_len)
+    c.ws = lib.new_workspace(c.batch, dense=True)
+    c.call(lib)
+    c.check()
+    assert lib.s5_get_device_error(c.ws)[0] == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("ctx,nq", [([5000, 64, 0], [1, 1, 1]), ([3000, 70], [4, 2])])
+def test_expired_wait_is_reported_and_the_next_call_is_right(lib, kv, ctx, nq):
+    """The test hook makes every CTA wait 1 ms for nothing: the call ends with S5_ERR_TIMEOUT."""
+    c = Case(ctx, nq, kv, seed=20, k_scale=1 / 64, v_scale=1 / 64).run(lib).check()
+    out = c.out.clone()
+    at = lib.S5_WS_TEST_STALL_OFFSET
+    c.ws[at:at + 8] = torch.tensor([1_000_000], dtype=torch.int64).view(torch.uint8).cuda()
+    c.call(lib)
+    torch.cuda.synchronize()
+    assert lib.s5_get_device_error(c.ws)[0] == lib.S5_ERR_TIMEOUT
+    lib.s5_reset_device_error(c.ws)
+    c.out.fill_(9.0)
+    c.call(lib)
+    assert torch.equal(c.out, out)
+    assert lib.s5_get_device_error(c.ws)[0] == 0
+
+
 def test_equals_sparse_attention_over_every_block(lib):
     """With every history block selected, the sparse layer's answer is the dense one."""
     c = Case([2000, 700], [1, 1], seed=18).run(lib).check()
