@@ -376,44 +376,66 @@ def s5_append_kv_fp8(k_pool, v_pool, key_pool, batch: Batch, k_new, v_new, key_n
                                  ws.numel(), _stream(stream)), "s5_append_kv_fp8")
 
 
-def _same_device(*tensors):
-    """The kernels run on the current device: every tensor has to be there."""
-    dev = torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+_I32, _BF16, _F32, _U8 = torch.int32, torch.bfloat16, torch.float32, torch.uint8
 
 
-def _dense_args(k_pool, v_pool, batch: Batch, q, out, lse, ws):
-    _need(q, torch.bfloat16, "q", (batch.total_q, N_HEADS, HEAD_DIM))
-    _need(out, torch.bfloat16, "out", (batch.total_q, N_HEADS, HEAD_DIM))
+def _ptrs(dtypes, names, *tensors):
+    """Addresses of contiguous tensors on the current device (the kernels run there),
+    None for None: one pass over the arguments of a call."""
+    dev, out = torch._C._cuda_getDevice(), []
+    try:
+        for t, dtype in zip(tensors, dtypes):
+            if t is None:
+                out.append(None)
+            elif t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+                out.append(t.data_ptr())
+            else:
+                break
+        else:
+            return out
+    except AttributeError:  # not a tensor
+        pass
+    i = len(out)
+    _need(tensors[i], dtypes[i], names[i])
+    raise ValueError(f"{names[i]} is on cuda:{tensors[i].get_device()}, the current device is cuda:{dev}")
+
+
+def _shape(t: torch.Tensor, shape, name: str):
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _dense(entry, where: str, dtype, k_pool, v_pool, batch: Batch, q, scales, out, lse, ws, stream):
+    if k_pool is None or v_pool is None or q is None or out is None or ws is None:
+        raise TypeError("k_pool, v_pool, q, out and ws must be CUDA tensors")
+    k, v, qp, op, lp, wp, _ = _ptrs((dtype, dtype, _BF16, _BF16, _F32, _U8, _I32),
+                                    ("k_pool", "v_pool", "q", "out", "lse", "ws", "page_table"),
+                                    k_pool, v_pool, q, out, lse, ws, batch.page_table)
+    sh, rows = k_pool.shape, (batch.total_q, N_HEADS, HEAD_DIM)
+    if len(sh) != 4:
+        raise ValueError(f"k_pool has shape {tuple(sh)}, expected [num_pages][4][64][192]")
+    _shape(v_pool, sh, "v_pool")
+    _shape(q, rows, "q")
+    _shape(out, rows, "out")
     if lse is not None:
-        _need(lse, torch.float32, "lse", (batch.total_q, N_HEADS))
-    _need(ws, torch.uint8, "ws")
-    _same_device(k_pool, v_pool, batch.page_table, q, out, lse, ws)
+        _shape(lse, rows[:2], "lse")
+    kv = KvDesc(k, v, sh[0], sh[2], sh[1], sh[3])
+    _check(entry(ctypes.byref(kv), ctypes.byref(batch.desc), qp, *scales, op, lp, wp, ws.numel(), _stream(stream)), where)
 
 
 def s5_dense_gqa_attn(k_pool, v_pool, batch: Batch, q, sm_scale: float, out, lse, ws, stream=None):
     """Attention of the batch's new tokens over the whole cache (positions 0 .. t
     of each row); ``lse`` may be None.  ``ws``: ``new_workspace(batch, dense=True)``."""
-    kv = _kv(k_pool, v_pool)
-    _dense_args(k_pool, v_pool, batch, q, out, lse, ws)
-    _check(_lib.s5_dense_gqa_attn(ctypes.byref(kv), ctypes.byref(batch.desc), _ptr(q), float(sm_scale), _ptr(out),
-                                  _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "s5_dense_gqa_attn")
+    _dense(_lib.s5_dense_gqa_attn, "s5_dense_gqa_attn", torch.bfloat16, k_pool, v_pool, batch, q, (float(sm_scale),),
+           out, lse, ws, stream)
 
 
 def s5_dense_gqa_attn_fp8kv(k_pool, v_pool, batch: Batch, q, sm_scale: float, k_scale: float, v_scale: float,
                             out, lse, ws, stream=None):
     """s5_dense_gqa_attn over one-byte KV: k_pool / v_pool uint8 E4M3 codes
     [num_pages][4][64][192], a code standing for its value times k_scale / v_scale."""
-    _need(k_pool, torch.uint8, "k_pool")
-    _need(v_pool, torch.uint8, "v_pool", tuple(k_pool.shape))
-    sh = k_pool.shape
-    kv = KvDesc(k_pool.data_ptr(), v_pool.data_ptr(), sh[0], sh[2], sh[1], sh[3])
-    _dense_args(k_pool, v_pool, batch, q, out, lse, ws)
-    _check(_lib.s5_dense_gqa_attn_fp8kv(ctypes.byref(kv), ctypes.byref(batch.desc), _ptr(q), float(sm_scale),
-                                        float(k_scale), float(v_scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
-                                        _stream(stream)), "s5_dense_gqa_attn_fp8kv")
+    _dense(_lib.s5_dense_gqa_attn_fp8kv, "s5_dense_gqa_attn_fp8kv", torch.uint8, k_pool, v_pool, batch, q,
+           (float(sm_scale), float(k_scale), float(v_scale)), out, lse, ws, stream)
 
 
 def s5_build_batch(req_pages, req_ids, new_lens, free_pages, batch: Batch, slots, positions, pages_used, ws,
@@ -424,20 +446,26 @@ def s5_build_batch(req_pages, req_ids, new_lens, free_pages, batch: Batch, slots
     [num_reqs][stride] (which receives the pages taken from ``free_pages``), the
     request of each sequence ``req_ids`` [batch] (-1: empty), ``batch.ctx_lens``
     and ``new_lens`` [batch].  ``batch.total_q`` is the sum of the new tokens."""
+    if req_pages is None or req_ids is None or new_lens is None or free_pages is None or ws is None:
+        raise TypeError("req_pages, req_ids, new_lens, free_pages and ws must be CUDA tensors")
+    pages, ids, new, free, sl, pos, used, wp, _ = _ptrs(
+        (_I32, _I32, _I32, _I32, _I32, _I32, _I32, _U8, _I32),
+        ("req_pages", "req_ids", "new_lens", "free_pages", "slots", "positions", "pages_used", "ws", "page_table"),
+        req_pages, req_ids, new_lens, free_pages, slots, positions, pages_used, ws, batch.page_table)
     n, rows = batch.ctx_lens.shape, (batch.total_q,)
-    for name, t, shape in (("req_pages", req_pages, None), ("req_ids", req_ids, n), ("new_lens", new_lens, n),
-                           ("free_pages", free_pages, None), ("slots", slots, rows), ("positions", positions, rows),
-                           ("pages_used", pages_used, (1,))):
-        if t is not None or name in ("req_pages", "req_ids", "new_lens", "free_pages"):
-            _need(t, torch.int32, name, shape)
-    if req_pages.dim() != 2:
-        raise ValueError("req_pages must be [num_reqs][stride]")
-    _need(ws, torch.uint8, "ws")
-    _same_device(req_pages, req_ids, new_lens, free_pages, batch.page_table, slots, positions, pages_used, ws)
-    reqs = RequestDesc(req_pages.data_ptr(), free_pages.data_ptr(), req_pages.shape[0], req_pages.shape[1],
-                       free_pages.numel())
-    _check(_lib.s5_build_batch(ctypes.byref(reqs), _ptr(req_ids), _ptr(new_lens), ctypes.byref(batch.desc),
-                               _ptr(slots), _ptr(positions), _ptr(pages_used), _ptr(ws), ws.numel(),
+    _shape(req_ids, n, "req_ids")
+    _shape(new_lens, n, "new_lens")
+    if slots is not None:
+        _shape(slots, rows, "slots")
+    if positions is not None:
+        _shape(positions, rows, "positions")
+    if pages_used is not None:
+        _shape(pages_used, (1,), "pages_used")
+    sh = req_pages.shape
+    if len(sh) != 2 or free_pages.dim() != 1:
+        raise ValueError("req_pages must be [num_reqs][stride], free_pages [num_free]")
+    reqs = RequestDesc(pages, free, sh[0], sh[1], free_pages.numel())
+    _check(_lib.s5_build_batch(ctypes.byref(reqs), ids, new, ctypes.byref(batch.desc), sl, pos, used, wp, ws.numel(),
                                _stream(stream)), "s5_build_batch")
 
 

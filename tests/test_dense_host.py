@@ -90,3 +90,27 @@ def test_build_batch_refusals(s5):
     assert call(ws=None) == wsp and call(n=s5.S5_WS_FIXED_BYTES - 1) == wsp
     assert f(None, FAKE, FAKE, ctypes.byref(_batch(s5)), FAKE, FAKE, FAKE, FAKE, 1 << 20, None) == bad
     assert f(ctypes.byref(_req(s5)), FAKE, FAKE, None, FAKE, FAKE, FAKE, FAKE, 1 << 20, None) == bad
+
+
+def test_binding_refuses_bad_tensors(s5, monkeypatch):
+    """The binding's argument checks, on CPU tensors (device -1 stands for the current device)."""
+    import torch
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1)
+    x, y = torch.zeros(4, dtype=torch.int32), torch.zeros(4, 4, dtype=torch.int32)
+    ptrs = s5._ptrs((torch.int32,) * 3, ("a", "b", "c"), x, None, y)
+    assert ptrs == [x.data_ptr(), None, y.data_ptr()]
+    # a CPU tensor, a wrong type, a strided one, no tensor at all: _need names it
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    for bad in (x, torch.zeros(4), y.t(), 5, [1]):
+        with pytest.raises(TypeError, match="b must be a CUDA tensor"):
+            s5._ptrs((torch.int32,) * 2, ("a", "b"), None, bad)
+
+    class Elsewhere(torch.Tensor):  # passes for a tensor of another device
+        is_cuda = True
+
+        def get_device(self):
+            return 3
+
+    t = torch.zeros(4, dtype=torch.int32).as_subclass(Elsewhere)
+    with pytest.raises(ValueError, match="a is on cuda:3, the current device is cuda:0"):
+        s5._ptrs((torch.int32,), ("a",), t)
