@@ -21,11 +21,11 @@
 // read by one SM.  The second kernel takes about 4 us, part of it while the first
 // one's last CTAs still run.)
 //
-// One CTA works in chunks of two pages (128 tokens): warp 4 streams K and warp
-// 5 V, one TMA copy per page and KV group, through rings in shared memory; warp 6
+// One CTA works in chunks of two pages (128 tokens): a warp streams K and another
+// V, one TMA copy per page and KV group, through rings in shared memory; one warp
 // issues S^T = K Q^T (M = 128 tokens, N = heads of the tile) into tensor memory;
-// warps 0-3, one thread per token, turn a row of S^T into weights P and store
-// them as the N operand of O^T += V^T P^T, which warp 7 issues (M = 128 + 64
+// softmax warps, a thread per token (4 rows: two), turn a row of S^T into weights P and store
+// them as the N operand of O^T += V^T P^T, which a fourth warp issues (M = 128 + 64
 // dims); O^T stays in tensor memory until the tile's run of pages ends.
 //
 // Tokens and dims are the M side so that no product is wasted: a decode row has
@@ -50,18 +50,19 @@ namespace s5 {
 
 namespace {
 
-constexpr int kDnSoft = 128;  // softmax threads: warps 0-3
-constexpr int kDnThreads = 256;
-constexpr int kWarpK = 4, kWarpV = 5, kWarpS = 6, kWarpPv = 7;
 constexpr int kChunk = 2 * kPage;                // tokens
 constexpr int kScanPer = 4;                      // sequences per thread and round of the prefix sums
-constexpr int kScanSeqs = kDnThreads * kScanPer;
 constexpr uint64_t kDnWaitNs = 2000000000ull;    // 2 s per wait
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <bool KV8, int RT>
 struct Cfg {
   static constexpr int kPairs = RT * kHpg;            // (row, head) pairs of a tile: columns of S^T and O^T
+  // Softmax warps: 4, a thread per token, or (4 rows) 8, two threads per token with half of the columns each
+  // (one thread's 64 columns took 3,500 cycles a chunk, one-byte KV: 16 x 16,384 tokens 120 us).
+  static constexpr int kSoftWarps = RT >= 2 ? 8 : 4, kSoft = 32 * kSoftWarps, kThreads = kSoft + 128;
+  static constexpr int kHalves = kSoftWarps / 4, kCols = kPairs / kHalves;  // threads per token, their columns
+  static constexpr int kWarpK = kSoftWarps, kWarpV = kWarpK + 1, kWarpS = kWarpK + 2, kWarpPv = kWarpK + 3;
   static constexpr int kQTerms = KV8 ? 2 : 1;         // terms of q (rows of the N operand)
   static constexpr int kS = kPairs * kQTerms;         // columns of S^T
   static constexpr int kTerms = KV8 ? (RT == 4 ? 3 : 4) : 2;
@@ -88,7 +89,7 @@ struct Cfg {
   static constexpr int kPRow = kP * (KV8 ? 1 : 2);
   static constexpr int kAtom = kPRow % 128 == 0 ? 128 : 64;
   static constexpr int kPGroup = 8 * kPRow;
-  static constexpr int kPBuf = RT == 1 || (KV8 && RT == 2) ? 2 : 1;   // buffers
+  static constexpr int kPBuf = KV8 || RT <= 2 ? 2 : 1;                  // buffers
   // Q: [3 planes][kS rows][kRowB]
   static constexpr int kQPlane = kS * kRowB;
   // the reference sits kOff binades under the maximum it was taken from and moves when a weight
@@ -110,7 +111,7 @@ struct Cfg {
   static constexpr int kOffMisc = kOffBar + (kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kSmem = kOffMisc + 128 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-  static_assert(16 * kPGroup >= kScanSeqs * 4, "the list of bad sequences lies in P's room");
+  static_assert(16 * kPGroup >= kThreads * kScanPer * 4, "the list of bad sequences lies in P's room");
 };
 
 // ---------------------------------------------------------------- the list of page units
@@ -295,19 +296,23 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
 
 // Barrier of the softmax warps (named barrier 1).  They always run the same sequence
 // of these: a warp whose bounded wait expired goes on to the next one, where all learn of it.
-__device__ __forceinline__ bool soft_or(bool x) {
+template <int THREADS>
+__device__ __forceinline__ bool soft_or_n(bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 1, 128, p;\n\t"
+      "bar.red.or.pred q, 1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)x)
+      : "r"((uint32_t)x), "n"(THREADS)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void soft_sync_n() {
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
 
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -329,14 +334,16 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_
 
 // The tile's queries as the N operand, K-major: row j * 16 + h; thread `tid` takes a run of
 // dims of one row.  bf16: as they are.  One byte: two E4M3 terms (rows n and kPairs + n) of q
-// times a power of two that puts the row's largest magnitude in [2^7, 2^8): the nearest code
-// and 16 times the remainder, together a bf16's 8 bits exactly down to 2^-14 of the largest
-// magnitude (smaller values are rounded to multiples of 2^-21 of it).  Returns the factor that
-// scores of the row are to be multiplied by (for every thread of the row).
+// times a power of two that puts the tile's largest finite magnitude in [2^7, 2^8): the nearest
+// code and 16 times the remainder, together a bf16's 8 bits exactly down to 2^-14 of that
+// magnitude; smaller values are rounded to multiples of 2^-21 of it, which changes a score by at
+// most 2^-22 of what the largest magnitude makes of the same K.  (One power per row instead
+// needs a factor per column in the softmax.)  Returns the factor of the scores.
 template <bool KV8, int RT>
-__device__ __forceinline__ float load_q(const DenseArgs &a, int row0, int nr, int g, uint8_t *sq, int tid) {
+__device__ __forceinline__ float load_q(const DenseArgs &a, int row0, int nr, int g, uint8_t *sq, float *max_s,
+                                        int tid) {
   using C = Cfg<KV8, RT>;
-  constexpr int kPer = kDnSoft / C::kPairs;  // threads per row
+  constexpr int kPer = C::kSoft / C::kPairs;  // threads per row
   constexpr int kPieces = kD / 8 / kPer;     // 8-dim pieces per thread
   const int n = tid / kPer, part = tid % kPer;
   const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale's sign goes into q
@@ -363,15 +370,19 @@ __device__ __forceinline__ float load_q(const DenseArgs &a, int row0, int nr, in
       for (int y = 0; y < 4; ++y) {
         const float f0 = fabsf(bf16lo(w[y])), f1 = fabsf(bf16hi(w[y]));
         finite = finite && f0 < INFINITY && f1 < INFINITY;
-        top = max3(top, f0, f1);
+        top = max3(top, f0 < INFINITY ? f0 : 0.f, f1 < INFINITY ? f1 : 0.f);
       }
     }
 #pragma unroll
-    for (int o = 1; o < kPer; o <<= 1) {
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      finite = __shfl_xor_sync(0xffffffffu, (int)finite, o) != 0 && finite;
-    }
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+    for (int o = 1; o < kPer; o <<= 1) finite = __shfl_xor_sync(0xffffffffu, (int)finite, o) != 0 && finite;
+    if (tid % 32 == 0) max_s[tid / 32] = top;
+    soft_sync_n<C::kSoft>();
+#pragma unroll
+    for (int i = 0; i < C::kSoftWarps; ++i) top = fmaxf(top, max_s[i]);
     const int e = (int)(__float_as_uint(top) >> 23);  // biased exponent of the largest magnitude
+    // (a row with a value that is not finite: NaN)
     float up = finite ? __uint_as_float((uint32_t)min(261 - e, 254) << 23) : __uint_as_float(0x7FC00000u);
     const float down = e > 7 ? __uint_as_float((uint32_t)(e - 7) << 23) : __uint_as_float(0x00400000u);
     if (flip) up = -up;
@@ -421,7 +432,7 @@ __device__ __forceinline__ void clean_v(uint8_t *vb, uint32_t *bad_s, bool page_
   using C = Cfg<KV8, RT>;
   constexpr int kPieces = C::kRowB / 16;  // 16-byte pieces of a token in a plane
   const int from = page_ok ? max(t0 + 1, 0) : 0;
-  for (int i = from * 3 * kPieces + tid; i < kPage * 3 * kPieces; i += kDnSoft) {
+  for (int i = from * 3 * kPieces + tid; i < kPage * 3 * kPieces; i += C::kSoft) {
     const int tok = i / (3 * kPieces), z = i % (3 * kPieces), plane = z / kPieces, pc = z % kPieces;
     uint4 *at = reinterpret_cast<uint4 *>(vb + (tok >> 3) * C::kGroup + plane * C::kPlane + (tok & 7) * C::kRowB + pc * 16);
     if (!page_ok || tok > t_last) {
@@ -451,15 +462,16 @@ __device__ __forceinline__ void clean_v(uint8_t *vb, uint32_t *bad_s, bool page_
 // ---------------------------------------------------------------- the kernel
 
 template <bool KV8, int RT>
-__global__ void __launch_bounds__(kDnThreads, 1)
+__global__ void __launch_bounds__(Cfg<KV8, RT>::kThreads, 1)
     dense_kernel(const DenseArgs a, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<KV8, RT>;
-  constexpr int KS = C::kKStages, VP = C::kVPages, PB = C::kPageBytes, NQ = C::kPairs;
+  constexpr int KS = C::kKStages, VP = C::kVPages, PB = C::kPageBytes, NQ = C::kPairs, NT = C::kThreads;
+  constexpr int kWarpK = C::kWarpK, kWarpV = C::kWarpV, kWarpS = C::kWarpS, kWarpPv = C::kWarpPv;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sk = smem, *sv = smem + C::kOffV, *sq = smem + C::kOffQ, *sp = smem + C::kOffP;
   float *col_s = reinterpret_cast<float *>(smem + C::kOffCol);
-  float *ref_s = col_s, *scale_s = col_s + NQ;                  // reference (0: none yet), score scale
+  float *ref_s = col_s, *max_s = col_s + NQ;                    // reference (0: none yet); warps' largest |q|
   float *warp_s = col_s + 2 * NQ;                               // [4][NQ]: the warps' maxima or sums
   // what a move of the reference changes (thread i reads column i of warp_s, then writes there)
   float *shift_s = warp_s, *corr_s = warp_s + NQ;
@@ -473,7 +485,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
   int *abort_flag = reinterpret_cast<int *>(smem + C::kOffMisc + 4);
   int *n_bad_s = reinterpret_cast<int *>(smem + C::kOffMisc + 12);
   Start *start_s = reinterpret_cast<Start *>(smem + C::kOffMisc + 16);
-  long long *sum_s = reinterpret_cast<long long *>(smem + C::kOffMisc + 64);  // [8]
+  long long *sum_s = reinterpret_cast<long long *>(col_s);                    // [warps], before the pipeline runs
   int *bad_list = reinterpret_cast<int *>(sp);                                // [kScanSeqs], before the pipeline runs
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -482,13 +494,13 @@ __global__ void __launch_bounds__(kDnThreads, 1)
     for (int i = 0; i < 2 * KS + 2 * VP; ++i) mbar_init(bars + i, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
-      mbar_init(s_empty + i, 4);
-      mbar_init(p_full + i, 4);
+      mbar_init(s_empty + i, C::kSoftWarps);
+      mbar_init(p_full + i, C::kSoftWarps);
       mbar_init(p_free + i, 1);
     }
-    mbar_init(q_full, 4);
+    mbar_init(q_full, C::kSoftWarps);
     mbar_init(q_empty, 1);
-    mbar_init(o_empty, 4);
+    mbar_init(o_empty, C::kSoftWarps);
     mbar_init(b_final, 2);
     mbar_init(b_stall, 1);
     *abort_flag = 0;
@@ -505,8 +517,8 @@ __global__ void __launch_bounds__(kDnThreads, 1)
   if (tid == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
 
   // ---- this CTA's share: prefix sums of the sequences' page units ----
-  const int per = a.batch <= kDnThreads ? 1 : kScanPer;  // sequences per thread
-  const int rounds = (a.batch + kDnThreads * per - 1) / (kDnThreads * per);
+  const int per = a.batch <= NT ? 1 : kScanPer;  // sequences per thread
+  const int rounds = (a.batch + NT * per - 1) / (NT * per);
   long long total = 0, units[kScanPer], before = 0;
   Seq seqs[kScanPer];
   auto scan_round = [&](int r, bool report) {  // units[] of this thread's sequences; exclusive prefix in `before`
@@ -514,14 +526,14 @@ __global__ void __launch_bounds__(kDnThreads, 1)
     bool any_bad = false;
 #pragma unroll
     for (int i = 0; i < kScanPer; ++i) {
-      const int s = (r * kDnThreads + tid) * per + i;
+      const int s = (r * NT + tid) * per + i;
       seqs[i].n = 0;
       seqs[i].bad = false;
       if (i < per && s < a.batch) seqs[i] = load_seq(a, s);
     }
 #pragma unroll
     for (int i = 0; i < kScanPer; ++i) {
-      const int s = (r * kDnThreads + tid) * per + i;
+      const int s = (r * NT + tid) * per + i;
         units[i] = kKv * group_units<RT, C::kStart>(seqs[i]);
       mine += units[i];
       if (seqs[i].bad && report && s % (int)gridDim.x == (int)blockIdx.x) {
@@ -541,7 +553,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
     before = incl - mine;
     long long all = 0;
 #pragma unroll
-    for (int w = 0; w < kDnThreads / 32; ++w) {
+    for (int w = 0; w < NT / 32; ++w) {
       if (w < warp) before += sum_s[w];
       all += sum_s[w];
     }
@@ -550,10 +562,10 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       for (int b = 0; b < nb; ++b) {
         const int s = bad_list[b];
         const int lo = max(ld_cg(a.cu_q + s), 0), hi = min(ld_cg(a.cu_q + s + 1), a.total_q);
-        for (long long i = (long long)lo * kHeads * (kD / 8) + tid; i < (long long)hi * kHeads * (kD / 8); i += kDnThreads)
+        for (long long i = (long long)lo * kHeads * (kD / 8) + tid; i < (long long)hi * kHeads * (kD / 8); i += NT)
           reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(0, 0, 0, 0);
         if (a.lse != nullptr)
-          for (long long i = (long long)lo * kHeads + tid; i < (long long)hi * kHeads; i += kDnThreads) a.lse[i] = -INFINITY;
+          for (long long i = (long long)lo * kHeads + tid; i < (long long)hi * kHeads; i += NT) a.lse[i] = -INFINITY;
       }
       __syncthreads();
       if (tid == 0) *n_bad_s = 0;
@@ -577,7 +589,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
 #pragma unroll
       for (int i = 0; i < kScanPer; ++i) {
         if (at <= u0 && u0 < at + units[i]) {
-          start_s->s = (r * kDnThreads + tid) * per + i;
+          start_s->s = (r * NT + tid) * per + i;
           start_s->off = u0 - at;
           start_s->q = seqs[i];
         }
@@ -762,17 +774,20 @@ __global__ void __launch_bounds__(kDnThreads, 1)
     }
     if (leader) tc::commit(b_final);
   } else {
-    // ---------------- softmax and epilogue: thread tid is token tid of the chunk, then dim tid ----------------
-    const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
+    // ---------------- softmax and epilogue: a thread is token tok of the chunk, then dim tok ----------------
+    constexpr int NC = C::kCols;  // its columns, from c0
+    const int tok = (warp & 3) * 32 + lane, half = warp >> 2, c0 = half * NC;
+    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    auto soft_or = [](bool v) { return soft_or_n<C::kSoft>(v); };
+    auto soft_sync = [] { soft_sync_n<C::kSoft>(); };
     int gc = 0, vp = 0, qi = 0;  // chunks, V pages, runs so far
     bool ok = true;              // this warp's waits so far; all four decide at the barriers
     // Q of a run, once the products of the run before have read theirs
     float scale = 0.f;
     auto stage_q = [&](const Seg &y) {
-      scale = fmaxf(load_q<KV8, RT>(a, y.row0, y.nr, y.g, sq, tid), 1e-37f);
+      scale = fmaxf(load_q<KV8, RT>(a, y.row0, y.nr, y.g, sq, max_s, tid), 1e-37f);
       // (a scale of 0 must not make a score of -inf NaN)
       fence_proxy_async_smem();
-      if (tid % (kDnSoft / NQ) == 0) scale_s[tid / (kDnSoft / NQ)] = scale;
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
     };
@@ -788,9 +803,9 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         ok = false;
         break;
       }
-      float2 l[NQ / 2];
+      float2 l[NC / 2];
 #pragma unroll
-      for (int i = 0; i < NQ / 2; ++i) l[i] = make_float2(0.f, 0.f);
+      for (int i = 0; i < NC / 2; ++i) l[i] = make_float2(0.f, 0.f);
       bool force = true;  // some column has no reference yet
       const int32_t *pt = a.page_table + (size_t)x.s * a.max_pages + x.p0;
       int nxt = lane < x.np ? ld_cg(pt + lane) : -1;
@@ -804,21 +819,26 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         const int base = (x.p0 + c) * kPage;
         const bool masked = !ok_a || !ok_b || base + kChunk - 1 > x.t0;
         const int sb = gc % C::kSBuf;
+        // (the references are fetched before the wait: while products run, they take most of shared
+        // memory's bandwidth, and these loads took 800 cycles of a 4-row tile's chunk after it)
+        float4 ref[NC / 4];
+#pragma unroll
+        for (int i = 0; i < NC / 4; ++i) ref[i] = *reinterpret_cast<const float4 *>(ref_s + c0 + 4 * i);
         ok = ok && wait(s_full + sb, (gc / C::kSBuf) & 1);
         __syncwarp();
         tc::fence_after_sync();
         // the token's scores, two columns per element
-        float2 sc[NQ / 2];
+        float2 sc[NC / 2];
         {
-          const uint32_t ts = tl + sb * C::kS;
+          const uint32_t ts = tl + sb * C::kS + c0;
           if constexpr (!KV8) {
 #pragma unroll
-            for (int i = 0; i < NQ / 16; ++i)
+            for (int i = 0; i < NC / 16; ++i)
               tc::ld_16cols(ts + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(reinterpret_cast<uint32_t *>(sc) + 16 * i));
             tc::wait_ld();
           } else {
 #pragma unroll
-            for (int i = 0; i < NQ / 16; ++i) {
+            for (int i = 0; i < NC / 16; ++i) {
               uint32_t lo[16];
               tc::ld_16cols(ts + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(reinterpret_cast<uint32_t *>(sc) + 16 * i));
               tc::ld_16cols(ts + NQ + 16 * i, lo);
@@ -834,22 +854,20 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(s_empty + sb);
         if (masked) {
-          const int pos = (tid < kPage ? ok_a : ok_b) ? base + tid : 0x7fffffff;
+          const int pos = (tok < kPage ? ok_a : ok_b) ? base + tok : 0x7fffffff;
 #pragma unroll
-          for (int j = 0; j < RT; ++j)
-            if (pos > min(x.t0 + j, t_last))
+          for (int j = 0; j < NC / kHpg; ++j)
+            if (pos > min(x.t0 + c0 / kHpg + j, t_last))
 #pragma unroll
               for (int i = 0; i < 8; ++i) sc[8 * j + i] = make_float2(-INFINITY, -INFINITY);
         }
         // relative to the references, in log2 units
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < NQ / 2; i += 2) {
-          const float4 r = *reinterpret_cast<const float4 *>(ref_s + 2 * i);
-          float4 w = make_float4(scale, scale, scale, scale);
-          if constexpr (KV8) w = *reinterpret_cast<const float4 *>(scale_s + 2 * i);
-          sc[i] = fma2(sc[i], make_float2(w.x, w.y), make_float2(-r.x, -r.y));
-          sc[i + 1] = fma2(sc[i + 1], make_float2(w.z, w.w), make_float2(-r.z, -r.w));
+        for (int i = 0; i < NC / 2; i += 2) {
+          const float4 r = ref[i / 2];
+          sc[i] = fma2(sc[i], make_float2(scale, scale), make_float2(-r.x, -r.y));
+          sc[i + 1] = fma2(sc[i + 1], make_float2(scale, scale), make_float2(-r.z, -r.w));
           mx[0] = max3(mx[0], sc[i].x, sc[i].y);
           mx[1] = max3(mx[1], sc[i + 1].x, sc[i + 1].y);
         }
@@ -857,10 +875,10 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         if (soft_or(force || !ok || fmaxf(mx[0], mx[1]) > C::kTop)) {
           // maxima of the columns over the chunk's tokens
 #pragma unroll
-          for (int i = 0; i < NQ; ++i) {
+          for (int i = 0; i < NC; ++i) {
             int b = __float_as_int(fmaxf((i & 1) ? sc[i / 2].y : sc[i / 2].x, -INFINITY));  // (NaN: -inf)
             b = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
-            if (lane == (i & 31)) warp_s[warp * NQ + i] = __int_as_float(b ^ ((b >> 31) & 0x7fffffff));
+            if (lane == i) warp_s[(warp & 3) * NQ + c0 + i] = __int_as_float(b ^ ((b >> 31) & 0x7fffffff));
           }
           if (soft_or(!ok)) {
             ok = false;
@@ -879,9 +897,9 @@ __global__ void __launch_bounds__(kDnThreads, 1)
           }
           force = soft_or(none);
 #pragma unroll
-          for (int i = 0; i < NQ / 2; ++i) {
-            const float2 sh = *reinterpret_cast<const float2 *>(shift_s + 2 * i);
-            const float2 co = *reinterpret_cast<const float2 *>(corr_s + 2 * i);
+          for (int i = 0; i < NC / 2; ++i) {
+            const float2 sh = *reinterpret_cast<const float2 *>(shift_s + c0 + 2 * i);
+            const float2 co = *reinterpret_cast<const float2 *>(corr_s + c0 + 2 * i);
             sc[i] = add2(sc[i], make_float2(-sh.x, -sh.y));
             l[i].x *= co.x;
             l[i].y *= co.y;
@@ -891,7 +909,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
             __syncwarp();
             tc::fence_after_sync();
 #pragma unroll 1
-            for (int cb = 0; cb < 2 * C::kP / 16; ++cb) {
+            for (int cb = half; cb < 2 * C::kP / 16; cb += C::kHalves) {
               uint32_t o[16];
               tc::ld_16cols(tl + C::kTmO + cb * 16, o);
               tc::wait_ld();
@@ -907,18 +925,18 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         const int pbuf = gc % C::kPBuf;
         if (gc >= C::kPBuf) ok = ok && wait(p_free + pbuf, (gc / C::kPBuf - 1) & 1);
         {
-          uint8_t *row = sp + pbuf * 16 * C::kPGroup + (tid >> 3) * C::kPGroup + (tid & 7) * C::kAtom;
-          const int sw = C::kAtom == 128 ? tid & 7 : (tid >> 1) & 3;
+          uint8_t *row = sp + pbuf * 16 * C::kPGroup + (tok >> 3) * C::kPGroup + (tok & 7) * C::kAtom;
+          const int sw = C::kAtom == 128 ? tok & 7 : (tok >> 1) & 3;
           constexpr int kPer = C::kAtom / 16;  // 16-byte pieces of an atom's row
           auto piece = [&](int i) {
             return reinterpret_cast<uint4 *>(row + (i / kPer) * 8 * C::kAtom + (((i % kPer) ^ sw) << 4));
           };
-          constexpr int kCols = KV8 ? 16 : 8;  // columns of a piece
+          constexpr int kPc = KV8 ? 16 : 8;  // columns of a piece
 #pragma unroll
-          for (int i0 = 0; i0 < NQ; i0 += kCols) {
+          for (int i0 = 0; i0 < NC; i0 += kPc) {
             uint32_t w[C::kTerms][4];
 #pragma unroll
-            for (int i = 0; i < kCols; i += KV8 ? 4 : 2) {
+            for (int i = 0; i < kPc; i += KV8 ? 4 : 2) {
               float2 p2[2];
 #pragma unroll
               for (int y = 0; y < (KV8 ? 2 : 1); ++y) {
@@ -950,7 +968,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
             }
 #pragma unroll
             for (int t = 0; t < C::kTerms; ++t)
-              *piece((t * NQ + i0) / kCols) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+              *piece((t * NQ + c0 + i0) / kPc) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
           }
         }
         if (masked) {
@@ -981,15 +999,15 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         walk.run(y);
         stage_q(y);
       }
-      // column sums over the warp: halves of the columns are exchanged until a lane has one (NQ = 64: two)
+      // column sums over the warp: halves of the columns are exchanged until a lane has one
       {
-        float v[NQ];
+        float v[NC];
 #pragma unroll
-        for (int i = 0; i < NQ / 2; ++i) {
+        for (int i = 0; i < NC / 2; ++i) {
           v[2 * i] = l[i].x;
           v[2 * i + 1] = l[i].y;
         }
-        int n = NQ, at = 0;
+        int n = NC, at = 0;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) {
           if (n > 1) {
@@ -997,7 +1015,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
             const bool up = (lane & o) != 0;
             if (up) at += n;
 #pragma unroll
-            for (int i = 0; i < NQ / 2; ++i)
+            for (int i = 0; i < NC / 2; ++i)
               if (i < n) v[i] = (up ? v[i + n] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + n], o);
           } else {
             v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
@@ -1005,8 +1023,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         }
         // the last products: once they are done, no warp reads what a moved reference left in warp_s
         ok = ok && wait(p_free + (gc - 1) % C::kPBuf, ((gc - 1) / C::kPBuf) & 1);
-        warp_s[warp * NQ + at] = v[0];
-        if constexpr (NQ == 64) warp_s[warp * NQ + at + 1] = v[1];
+        warp_s[(warp & 3) * NQ + c0 + at] = v[0];
       }
       if (soft_or(!ok)) {
         ok = false;
@@ -1035,17 +1052,17 @@ __global__ void __launch_bounds__(kDnThreads, 1)
       }
       soft_sync();
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {  // dims 0-127, then 128-191 (M = 64: 16 lanes of every warp)
-        const int d = half == 0 ? tid : 128 + warp * 16 + lane;
-        const bool on = half == 0 || lane < 16;
+      for (int part = 0; part < 2; ++part) {  // dims 0-127, then 128-191 (M = 64: 16 lanes of a lane quarter)
+        const int d = part == 0 ? tok : 128 + (warp & 3) * 16 + lane;
+        const bool on = part == 0 || lane < 16;
         const uint32_t nf = on ? bad_s[d >> 2] >> (8 * (d & 3)) : 0;  // bit j: row j saw a value that is not finite
 #pragma unroll 1
-        for (int j = 0; j < x.nr; ++j) {
+        for (int j = c0 / kHpg; j < min(x.nr, (c0 + NC) / kHpg); ++j) {
           float v[16];
           uint32_t o[C::kTerms][16];
 #pragma unroll
           for (int t = 0; t < C::kTerms; ++t)
-            tc::ld_16cols(tl + (half == 0 ? C::kTmO : C::kTmO2) + t * NQ + j * 16, o[t]);
+            tc::ld_16cols(tl + (part == 0 ? C::kTmO : C::kTmO2) + t * NQ + j * 16, o[t]);
           tc::wait_ld();
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -1249,7 +1266,7 @@ cudaError_t launch(const DenseArgs &a, const CUtensorMap &tk, const CUtensorMap 
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.n_ctas);
-  cfg.blockDim = dim3(kDnThreads);
+  cfg.blockDim = dim3(Cfg<KV8, RT>::kThreads);
   cfg.dynamicSmemBytes = Cfg<KV8, RT>::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
