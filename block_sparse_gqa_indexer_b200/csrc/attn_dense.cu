@@ -8,25 +8,27 @@
 //   M = max_p m_p,  O = sum_p 2^(m_p - M) O_p,  L = sum_p 2^(m_p - M) l_p.
 //
 // Bound: HBM.  A cached token costs 3,072 bytes (bf16) for 16 FLOPs per byte and
-// query row, far below the tensor cores' ratio even for the 8 rows of a tile, so
-// the aim is a full stream of pages on every SM.
+// query row, far below the tensor cores' ratio even for the 4 rows of a tile, so
+// the aim is a full stream of pages on every SM: 32 requests x 131,072 bf16 tokens
+// take 1.80 ms = 7.2 TB/s, 64 x 49,000 one-byte tokens 0.70 to 0.76 ms = 6.7 to 6.2.
 //
 // Split.  The work is a list of page units: sequences in order, in each its KV
 // groups, in each group its tiles of `tile_rows` query rows, in each tile the
 // pages up to its last row.  Every CTA (one per SM, persistent) finds its equal
 // share of the list from the device's lengths by prefix sums, so ragged batches
 // balance to within a page and one long sequence spreads over every SM.  A tile
-// that spans CTAs leaves a part per CTA, and a second kernel joins the parts.  (Joined by the last CTA to arrive, in two levels, a tile
-// of 37 parts took 14 us, 4 rows 21 us: two counters' round trips and the parts
-// read by one SM.  The second kernel takes about 4 us, part of it while the first
-// one's last CTAs still run.)
+// that spans CTAs leaves a part per CTA, and a second kernel joins the parts.
+// (Joined by the last CTA to arrive, in two levels, a tile of 37 parts took 14 us,
+// of 4 rows 21 us: two counters' round trips, and the parts read by one SM.  The
+// second kernel takes about 5 us.)
 //
 // One CTA works in chunks of two pages (128 tokens): a warp streams K and another
 // V, one TMA copy per page and KV group, through rings in shared memory; one warp
 // issues S^T = K Q^T (M = 128 tokens, N = heads of the tile) into tensor memory;
-// softmax warps, a thread per token (4 rows: two), turn a row of S^T into weights P and store
-// them as the N operand of O^T += V^T P^T, which a fourth warp issues (M = 128 + 64
-// dims); O^T stays in tensor memory until the tile's run of pages ends.
+// the softmax warps, a thread per token (2 or 4 rows: two), turn a row of S^T into
+// weights P and store them as the N operand of O^T += V^T P^T, which a fourth warp
+// issues (M = 128 + 64 dims); O^T stays in tensor memory until the tile's run of
+// pages ends.
 //
 // Tokens and dims are the M side so that no product is wasted: a decode row has
 // only 16 heads per KV group, and with heads as M = 128 rows (copies of the heads
@@ -58,8 +60,8 @@ constexpr float kLn2 = 0.69314718055994531f;
 template <bool KV8, int RT>
 struct Cfg {
   static constexpr int kPairs = RT * kHpg;            // (row, head) pairs of a tile: columns of S^T and O^T
-  // Softmax warps: 4, a thread per token, or (4 rows) 8, two threads per token with half of the columns each
-  // (one thread's 64 columns took 3,500 cycles a chunk, one-byte KV: 16 x 16,384 tokens 120 us).
+  // Softmax warps: 4, a thread per token, or (2 and 4 rows) 8, two threads per token with half of the
+  // columns each (one-byte KV, 16 x 16,384 tokens, 2 rows: 80 against 73 us; 4 rows: 121 against 93 us).
   static constexpr int kSoftWarps = RT >= 2 ? 8 : 4, kSoft = 32 * kSoftWarps, kThreads = kSoft + 128;
   static constexpr int kHalves = kSoftWarps / 4, kCols = kPairs / kHalves;  // threads per token, their columns
   static constexpr int kWarpK = kSoftWarps, kWarpV = kWarpK + 1, kWarpS = kWarpK + 2, kWarpPv = kWarpK + 3;
@@ -79,9 +81,9 @@ struct Cfg {
   static constexpr int kRowB = KV8 ? 64 : 128;
   static constexpr int kPlane = 8 * kRowB;
   static constexpr int kGroup = 3 * kPlane;
-  // Rings of 172 KB (one byte: 123 KB).  Deeper ones do not stream faster but less evenly: with four V pages (bf16)
-  // the first SM ended 32 x 131,072 tokens 180 us before the last and the call took 1.89 ms, with
-  // three 1.83 ms.
+  // Rings of 172 KB (one byte: 123 KB).  Deeper ones do not stream faster but less evenly: with four
+  // V pages (bf16) the first SM ended 32 x 131,072 tokens 180 us before the last and the call took
+  // 1.89 ms, with three 1.83 ms.
   static constexpr int kKStages = KV8 ? 3 : 2;                        // chunks in the K ring
   static constexpr int kVPages = KV8 ? 4 : 3;                         // pages in the V ring
   static constexpr int kChunkBytes = 2 * kPageBytes;
@@ -89,7 +91,7 @@ struct Cfg {
   static constexpr int kPRow = kP * (KV8 ? 1 : 2);
   static constexpr int kAtom = kPRow % 128 == 0 ? 128 : 64;
   static constexpr int kPGroup = 8 * kPRow;
-  static constexpr int kPBuf = KV8 || RT <= 2 ? 2 : 1;                  // buffers
+  static constexpr int kPBuf = KV8 || RT <= 2 ? 2 : 1;  // buffers (bf16, 4 rows: no room for two)
   // Q: [3 planes][kS rows][kRowB]
   static constexpr int kQPlane = kS * kRowB;
   // the reference sits kOff binades under the maximum it was taken from and moves when a weight
@@ -97,14 +99,14 @@ struct Cfg {
   // weights of 2^-28 of the largest still count.
   static constexpr float kOff = KV8 ? 12.f : 0.f;
   static constexpr float kTop = KV8 ? 15.f : 8.f;
-  // What a run costs besides its pages, in pages, for equal shares: 64 ragged requests' SMs took 2 us a
-  // run, 16 verified requests' (4 rows) 7 us.
+  // What a run costs besides its pages, in pages, for equal shares: 2 us a run were measured on 64 ragged
+  // requests (1 row), 7 us on 16 verified ones (4 rows); a bf16 page takes about 1 us.
   static constexpr int kStart = (RT == 1 ? 2 : RT == 2 ? 4 : 6) * (KV8 ? 2 : 1);
   // shared memory (from a 1,024-byte aligned base)
   static constexpr int kOffV = kKStages * kChunkBytes;
   static constexpr int kOffQ = kOffV + kVPages * kPageBytes;
   static constexpr int kOffP = kOffQ + 3 * kQPlane;
-  static constexpr int kOffCol = kOffP + kPBuf * 16 * kPGroup;                // float [6][kPairs]: per-column values
+  static constexpr int kOffCol = kOffP + kPBuf * 16 * kPGroup;        // float [6][kPairs]: per-column values
   static constexpr int kOffBad = kOffCol + 6 * kPairs * 4;            // uint32 [48]: per dim, rows that saw a non-finite value
   static constexpr int kOffBar = kOffBad + 192;
   static constexpr int kNumBars = 2 * kKStages + 2 * kVPages + 13;
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(Cfg<KV8, RT>::kThreads, 1)
   int *n_bad_s = reinterpret_cast<int *>(smem + C::kOffMisc + 12);
   Start *start_s = reinterpret_cast<Start *>(smem + C::kOffMisc + 16);
   long long *sum_s = reinterpret_cast<long long *>(col_s);                    // [warps], before the pipeline runs
-  int *bad_list = reinterpret_cast<int *>(sp);                                // [kScanSeqs], before the pipeline runs
+  int *bad_list = reinterpret_cast<int *>(sp);                                // [NT * kScanPer], before the pipeline runs
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -534,7 +536,7 @@ __global__ void __launch_bounds__(Cfg<KV8, RT>::kThreads, 1)
 #pragma unroll
     for (int i = 0; i < kScanPer; ++i) {
       const int s = (r * NT + tid) * per + i;
-        units[i] = kKv * group_units<RT, C::kStart>(seqs[i]);
+      units[i] = kKv * group_units<RT, C::kStart>(seqs[i]);
       mine += units[i];
       if (seqs[i].bad && report && s % (int)gridDim.x == (int)blockIdx.x) {
         record_error(a.err, S5_ERR_DEVICE_BOUNDS, max(seqs[i].lo, 0));
@@ -781,7 +783,7 @@ __global__ void __launch_bounds__(Cfg<KV8, RT>::kThreads, 1)
     auto soft_or = [](bool v) { return soft_or_n<C::kSoft>(v); };
     auto soft_sync = [] { soft_sync_n<C::kSoft>(); };
     int gc = 0, vp = 0, qi = 0;  // chunks, V pages, runs so far
-    bool ok = true;              // this warp's waits so far; all four decide at the barriers
+    bool ok = true;              // this thread's waits so far; all decide at the barriers
     // Q of a run, once the products of the run before have read theirs
     float scale = 0.f;
     auto stage_q = [&](const Seg &y) {

@@ -143,7 +143,7 @@ struct TileArgs {
 };
 
 // Dense attention over the whole cache.
-constexpr int kDenseMaxRows = 4;  // query rows per tile (4 rows x 16 heads x 4 terms = N 256)
+constexpr int kDenseMaxRows = 4;  // query rows per tile (tensor memory: 2 x 4 rows x 16 heads x 3 terms + scores)
 
 struct DenseArgs {
   int num_pages;

@@ -349,10 +349,11 @@ s5_status s5_dense_gqa_attn(const s5_kv_desc *kv, const s5_batch_desc *batch, co
 
 /* s5_dense_gqa_attn over one-byte KV: pools, codes and scales as in
  * s5_sparse_gqa_attn_fp8kv.  Products run on 8-bit tensor cores with the other
- * operand in terms: q as two E4M3 values of q times a power of two (exact for
- * bf16 values down to 2^-14 of the row and head's largest magnitude, smaller ones
- * to 2^-21 of it); a weight in f16 as E5M2 values, together exact (max_q <= 2) or
- * within 2^-9 of the weight, and to 2^-28 of the largest.  k_scale, v_scale and
+ * operand in terms: q as two E4M3 values of q times a power of two, exact for bf16
+ * values down to 2^-14 of the largest finite magnitude among the group's 16 heads
+ * and the rows computed together (up to 4 of a sequence), smaller ones to 2^-21 of
+ * it; a weight in f16 as E5M2 values, together exact (max_q <= 2) or within 2^-9 of
+ * the weight, and to 2^-28 of the largest.  k_scale, v_scale and
  * sm_scale * k_scale must be finite (S5_ERR_INVALID_ARG). */
 s5_status s5_dense_gqa_attn_fp8kv(const s5_kv_desc *kv, const s5_batch_desc *batch, const void *q, float sm_scale,
                                   float k_scale, float v_scale, void *out, float *lse, void *workspace,

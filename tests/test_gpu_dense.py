@@ -14,6 +14,8 @@ Tolerances, derived from the roundings of the computation.  With A = sum_j w_j |
                          a scaled, shifted score), in the sum and the quotient: twice that, times A
   long sums              n additions in fp32: 2^-24 n A at most; pieces of at
                          most n / 8 are added, then joined:  2^-27 n A + 2^-20 A
+One byte: q is held to 2^-21 of the largest magnitude Q of a group's heads in the rows computed
+together, so scores are off by another sm_scale * 2^-22 Q max_j sum_d |K_jd|.
 The lse adds the score error, 2^-20 and 2^-27 n, and its own rounding 2^-23 |lse|.
 """
 import math
@@ -118,6 +120,9 @@ class Case:
             out, a = term.sum(3), term.abs().sum(3)
         b = mag.masked_fill(~m, 0.0).amax(-1)
         score = 200 * 2.0 ** -24 * b + 2.0 ** -20
+        if self.kv == "fp8":
+            qmax = torch.where(torch.isfinite(q), q.abs(), 0.0).amax((0, 2, 3))
+            score = score + (2.0 ** -22 * abs(self.sm) * qmax * k.abs().sum(-1).amax(-1))[None, :, None]
         weight = 2.0 ** -8 if self.kv == "bf16" else 2.0 ** -11 if max(self.nq) <= 2 else 2.0 ** -9
         tol = 2.0 ** -8 * out.abs() + (weight + 2 * score + 2.0 ** -27 * n + 2.0 ** -20)[..., None] * a + 1e-30
         tol_lse = score + 2.0 ** -20 + 2.0 ** -27 * n + 2.0 ** -23 * lse.abs()
@@ -305,6 +310,32 @@ def test_one_heavy_token_and_many_light_ones(lib, kv, nq, at, gap):
 @pytest.mark.parametrize("sm", [0.0, -SM, 3.0])
 def test_scales(lib, kv, sm):
     Case([700, 64], [1, 4], kv, seed=10, k_scale=1 / 64, v_scale=-1 / 64, sm=sm).run(lib).check()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("nq", [1, 2, 4])
+def test_queries_of_very_different_size(lib, kv, nq):
+    """Heads of 1/256 and rows of 64 times the others' size, dims of 2^-20 and of zero."""
+    c = Case([900], [nq], kv, seed=21, k_scale=1 / 64, v_scale=1 / 64)
+    c.q[:, 5:64:9] *= 1 / 256
+    c.q[nq - 1] *= 64
+    c.q[:, :, 100:104] *= 2.0 ** -20
+    c.q[:, :, 150:] = 0
+    c.q[:, 33] = 0  # a head without a query: the mean of V
+    c.run(lib).check()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_a_query_that_is_not_finite_stays_in_its_row_and_head(lib, kv, bad):
+    c = Case([300], [4], kv, seed=22, k_scale=1 / 64, v_scale=1 / 64).run(lib)
+    out, lse = c.out.clone(), c.lse.clone()
+    c.q[2, 20, 7] = bad
+    c.call(lib)
+    keep = torch.ones((4, H), dtype=torch.bool, device="cuda")
+    keep[2, 20] = False
+    assert torch.equal(c.out[keep], out[keep]) and torch.equal(c.lse[keep], lse[keep])
+    assert not bool(torch.isfinite(c.out[2, 20]).any()) and not bool(torch.isfinite(c.lse[2, 20]))
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
