@@ -161,6 +161,7 @@ struct DenseArgs {
   int tile_rows;     // query rows per tile: 1, 2 or 4
   int reread;        // nonzero: sequences may have several tiles, which read the same pages
   int n_ctas;
+  int whole;         // nonzero: tiles are not split over CTAs
   void *out;
   float *lse;
   float *part_o;   // [2 * n_ctas][tile_rows * 16][192]

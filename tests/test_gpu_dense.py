@@ -171,6 +171,22 @@ def test_against_formula(lib, name, kv):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("name", [n for n, (ctx, nq) in BATCHES.items() if max(c + q for c, q in zip(ctx, nq)) <= 768])
+def test_short_sequences_in_a_batch_made_for_long_ones(lib, name, kv):
+    """max_len bounds the lengths from far above: tiles may be split over CTAs."""
+    ctx, nq = BATCHES[name]
+    need = max(pages(c + q) for c, q in zip(ctx, nq))
+    c = Case(ctx, nq, kv, seed=30 + len(name), extra_pages=40, k_scale=1 / 64, v_scale=1 / 64, max_len=(need + 40) * PAGE)
+    c.run(lib).check()
+    wide = c.out.clone()
+    d = Case(ctx, nq, kv, seed=30 + len(name), extra_pages=40, k_scale=1 / 64, v_scale=1 / 64).run(lib).check()
+    for s in range(len(ctx)):  # the same answers, however the work is divided
+        if nq[s]:
+            _, _, tol, _ = d.expect(s)
+            assert bool(((d.out - wide)[d.cu[s]:d.cu[s + 1]].double().abs() <= 2 * tol).all())
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_without_lse_and_repeatable(lib, kv):
     c = Case([5000, 100, 64], [1, 2, 8], kv, seed=3, k_scale=1 / 64, v_scale=1 / 64).run(lib).check()
     out, lse = c.out.clone(), c.lse.clone()
@@ -185,7 +201,7 @@ def test_without_lse_and_repeatable(lib, kv):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
-@pytest.mark.parametrize("hi,nq", [(300, 1), (4000, 1), (2500, 4)])
+@pytest.mark.parametrize("hi,nq", [(300, 1), (700, 8), (4000, 1), (2500, 4)])
 def test_ragged_batches_repeat_bit_for_bit(lib, kv, hi, nq):
     """Many sequences per CTA, runs of one chunk among them: right, and the same every time."""
     g = torch.Generator().manual_seed(hi)
