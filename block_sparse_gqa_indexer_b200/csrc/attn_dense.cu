@@ -525,9 +525,11 @@ __global__ void __launch_bounds__(Cfg<KV8, RT>::kThreads, 1)
   }
   if (tid < 48) bad_s[tid] = 0;
   fence_mbar_init();
-  __syncthreads();
   if (warp == kWarpPv) tc::tmem_alloc(tmem_slot, C::kTmCols);
-
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
   if (tid == kWarpK * 32) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
   if (tid == kWarpV * 32) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
   pdl_wait();  // (programmatic launch) global memory is read from here on
@@ -590,7 +592,29 @@ __global__ void __launch_bounds__(Cfg<KV8, RT>::kThreads, 1)
     if (rounds > 1) __syncthreads();  // sum_s and the list are written again
     return all;
   };
-  for (int r = 0; r < rounds; ++r) total += scan_round(r, true);
+  // Up to 32 sequences: every warp has the sums by itself, a lane per sequence, and none waits for
+  // another (a bad sequence, whose rows are to be filled, takes the other way)
+  Start start;
+  bool by_warp = false;
+  long long incl_w = 0, units_w = 0;
+  if (a.batch <= 32) {
+    start.q.n = 0;
+    start.q.bad = false;
+    if (lane < a.batch) start.q = load_seq(a, lane);
+    by_warp = !__any_sync(0xffffffffu, start.q.bad);
+    units_w = kKv * group_units<RT, C::kStart>(start.q);
+    incl_w = units_w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl_w, o);
+      if (lane >= o) incl_w += v;
+    }
+    total = __shfl_sync(0xffffffffu, incl_w, 31);
+  }
+  if (!by_warp) {
+    total = 0;
+    for (int r = 0; r < rounds; ++r) total += scan_round(r, true);
+  }
   long long chunk = total < (1LL << 31) ? max(((uint32_t)total + gridDim.x - 1) / gridDim.x, 1u)
                                         : (total + gridDim.x - 1) / gridDim.x;
   // (short shares take as long for a page as for a chunk, and have fewer parts to join)
@@ -598,7 +622,15 @@ __global__ void __launch_bounds__(Cfg<KV8, RT>::kThreads, 1)
   const long long u0 = chunk * blockIdx.x;
   const bool idle = u0 >= total;
   const long long count = min(chunk, total - u0);
-  if (!idle) {
+  if (by_warp) {
+    const int src = __popc(__ballot_sync(0xffffffffu, incl_w <= u0));  // sequences that end at or before u0
+    const long long off = u0 - (incl_w - units_w);
+    start.s = src;
+    start.off = __shfl_sync(0xffffffffu, off, src & 31);
+    start.q.lo = __shfl_sync(0xffffffffu, start.q.lo, src & 31);
+    start.q.n = __shfl_sync(0xffffffffu, start.q.n, src & 31);
+    start.q.ctx = __shfl_sync(0xffffffffu, start.q.ctx, src & 31);
+  } else if (!idle) {
     long long base = 0;
     for (int r = 0; r < rounds; ++r) {
       const long long all = rounds > 1 ? scan_round(r, false) : total;
@@ -616,15 +648,15 @@ __global__ void __launch_bounds__(Cfg<KV8, RT>::kThreads, 1)
       if (base > u0) break;
     }
   }
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
   if (idle) {
     if (warp == kWarpPv) tc::tmem_dealloc(tmem, C::kTmCols);
     return;
   }
-  Walk<RT, C::kStart> walk(a, start_s->q, start_s->s, start_s->off, u0, count);
+  if (!by_warp) {
+    __syncthreads();
+    start = *start_s;
+  }
+  Walk<RT, C::kStart> walk(a, start.q, start.s, start.off, u0, count);
   Seg x;
 
   // Bounded wait.  (Polling with test_wait instead, without suspension, was 3% slower: the
