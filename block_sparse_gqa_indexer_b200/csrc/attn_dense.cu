@@ -7,7 +7,7 @@
 // per (row, head); parts of a row's cache are joined by
 //   M = max_p m_p,  O = sum_p 2^(m_p - M) O_p,  L = sum_p 2^(m_p - M) l_p.
 //
-// Bound: HBM.  A cached token costs 3,072 bytes (bf16) for 16 FLOPs per byte and
+// Bound: HBM.  A cached token costs 3 KB (bf16) for 16 FLOPs per byte and
 // query row, far below the tensor cores' ratio even for the 4 rows of a tile, so
 // the aim is a full stream of pages on every SM: 32 requests x 131,072 bf16 tokens
 // take 1.80 ms = 7.2 TB/s, 64 x 49,000 one-byte tokens 0.70 to 0.76 ms = 6.7 to 6.2.
