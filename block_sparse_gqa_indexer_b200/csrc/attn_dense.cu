@@ -96,6 +96,7 @@ struct Cfg {
   static constexpr int kPBuf = KV8 || RT <= 2 ? 2 : 1;  // buffers (bf16, 4 rows: no room for two)
   // Q: [3 planes][kS rows][kRowB]
   static constexpr int kQPlane = kS * kRowB;
+  static constexpr int kQThreads = kSoft / kPairs, kQPieces = kD / 8 / kQThreads;  // threads of a row, 8-dim pieces of each
   // the reference sits kOff binades under the maximum it was taken from and moves when a weight
   // would exceed 2^kTop.  One byte: f16 weights reach 2^15, E5M2 ones go down to 2^-16, so
   // weights of 2^-28 of the largest still count.
@@ -357,18 +358,22 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_
 // most 2^-22 of what the largest magnitude makes of the same K.  (One power per row instead
 // needs a factor per column in the softmax.)  Returns the factor of the scores.
 template <bool KV8, int RT>
-__device__ __forceinline__ float load_q(const DenseArgs &a, int row0, int nr, int g, uint8_t *sq, float *max_s,
-                                        int tid) {
+__device__ __forceinline__ void fetch_q(const DenseArgs &a, const Seg &x, int tid, uint4 (&v)[Cfg<KV8, RT>::kQPieces]) {
   using C = Cfg<KV8, RT>;
-  constexpr int kPer = C::kSoft / C::kPairs;  // threads per row
-  constexpr int kPieces = kD / 8 / kPer;     // 8-dim pieces per thread
+  const int n = tid / C::kQThreads, part = tid % C::kQThreads;
+  const uint4 *src = reinterpret_cast<const uint4 *>(a.q) +
+                     ((size_t)(x.row0 + n / kHpg) * kHeads + x.g * kHpg + n % kHpg) * (kD / 8) + part * C::kQPieces;
+#pragma unroll
+  for (int i = 0; i < C::kQPieces; ++i) v[i] = n / kHpg < x.nr ? ld_cg(src + i) : make_uint4(0, 0, 0, 0);
+}
+
+template <bool KV8, int RT>
+__device__ __forceinline__ float store_q(const DenseArgs &a, const uint4 (&v)[Cfg<KV8, RT>::kQPieces], uint8_t *sq,
+                                         float *max_s, int tid) {
+  using C = Cfg<KV8, RT>;
+  constexpr int kPer = C::kQThreads, kPieces = C::kQPieces;
   const int n = tid / kPer, part = tid % kPer;
   const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale's sign goes into q
-  const uint4 *src = reinterpret_cast<const uint4 *>(a.q) +
-                     ((size_t)(row0 + n / kHpg) * kHeads + g * kHpg + n % kHpg) * (kD / 8) + part * kPieces;
-  uint4 v[kPieces];
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i) v[i] = n / kHpg < nr ? ld_cg(src + i) : make_uint4(0, 0, 0, 0);
   if constexpr (!KV8) {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
@@ -833,8 +838,10 @@ __global__ void __launch_bounds__(Cfg<KV8, RT>::kThreads, 1)
     bool ok = true;              // this thread's waits so far; all decide at the barriers
     // Q of a run, once the products of the run before have read theirs
     float scale = 0.f;
-    auto stage_q = [&](const Seg &y) {
-      scale = fmaxf(load_q<KV8, RT>(a, y.row0, y.nr, y.g, sq, max_s, tid), 1e-37f);
+    uint4 qv[C::kQPieces];
+    constexpr bool kEarlyQ = RT == 1;  // (registers for it: 3 pieces a thread)
+    auto stage_q = [&]() {
+      scale = fmaxf(store_q<KV8, RT>(a, qv, sq, max_s, tid), 1e-37f);
       // (a scale of 0 must not make a score of -inf NaN)
       fence_proxy_async_smem();
       __syncwarp();
@@ -842,7 +849,8 @@ __global__ void __launch_bounds__(Cfg<KV8, RT>::kThreads, 1)
     };
     if (walk.rem > 0) {
       walk.run(x);
-      stage_q(x);
+      fetch_q<KV8, RT>(a, x, tid, qv);
+      stage_q();
     }
     while (walk.next(x)) {
       const int t_last = x.t0 + x.nr - 1;
@@ -851,6 +859,11 @@ __global__ void __launch_bounds__(Cfg<KV8, RT>::kThreads, 1)
       if (soft_or(!ok)) {
         ok = false;
         break;
+      }
+      if (kEarlyQ && walk.rem > 0) {  // the next run's Q is under way during this one
+        Seg y;
+        walk.run(y);
+        fetch_q<KV8, RT>(a, y, tid, qv);
       }
       float2 l[NC / 2];
 #pragma unroll
@@ -1044,9 +1057,12 @@ __global__ void __launch_bounds__(Cfg<KV8, RT>::kThreads, 1)
       // ---- the run's result ----
       if (walk.rem > 0) {  // the next run's Q first, so that its first scores are there after this epilogue
         ok = ok && wait(q_empty, qi & 1);
-        Seg y;
-        walk.run(y);
-        stage_q(y);
+        if (!kEarlyQ) {
+          Seg y;
+          walk.run(y);
+          fetch_q<KV8, RT>(a, y, tid, qv);
+        }
+        stage_q();
       }
       // column sums over the warp: halves of the columns are exchanged until a lane has one
       {

@@ -123,6 +123,12 @@ def test_free_list_runs_out(lib):
     b.check()
 
 
+def test_no_free_pages_and_no_rows(lib):
+    Build(lib, [64, 10, 0], [0, 3, 0], n_free=0, seed=7).run(lib).check()
+    b = Build(lib, [64, 10], [0, 0], n_free=0, seed=8).run(lib).check()
+    assert b.total_q == 0 and b.batch.cu_q.tolist() == [0, 0, 0]
+
+
 def test_rows_beyond_total_q_are_cut(lib):
     b = Build(lib, [64, 10, 128], [3, 4, 2], total_q=5, seed=4).run(lib, code=lib.S5_ERR_DEVICE_BOUNDS)
     assert lib.s5_get_device_error(b.ws)[1] == 1

@@ -63,7 +63,7 @@ class Case:
         self.rows, self.total_q = self.cu[-1], self.cu[-1] + pad_rows
         self.q = torch.randn((self.total_q, H, D), generator=g, device="cuda").to(torch.bfloat16)
         self.max_len = max(c + n for c, n in zip(ctx, nq)) if max_len is None else max_len
-        self.max_q = max(nq)
+        self.max_q = max(1, *nq)
 
     def make(self, lib):
         i32 = dict(dtype=torch.int32, device="cuda")
@@ -225,6 +225,12 @@ def test_ragged_batches_repeat_bit_for_bit(lib, kv, hi, nq):
 def test_rows_behind_the_batch_stay(lib, kv):
     c = Case([500, 3], [2, 1], kv, seed=4, pad_rows=6, k_scale=1 / 64, v_scale=1 / 64).run(lib).check()
     assert bool((c.out[3:] == 7.0).all()) and bool((c.lse[3:] == 7.0).all())
+
+
+def test_a_padded_batch_without_a_sequence(lib):
+    """Rows, but no sequence has new tokens: nothing is written."""
+    c = Case([500, 0, 64], [0, 0, 0], seed=23, pad_rows=5, max_len=600, extra_pages=3).run(lib)
+    assert bool((c.out == 7.0).all()) and bool((c.lse == 7.0).all())
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
