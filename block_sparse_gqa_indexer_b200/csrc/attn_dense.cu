@@ -507,6 +507,7 @@ __global__ void __launch_bounds__(Cfg<KV8, RT>::kThreads, 1)
   int *abort_flag = reinterpret_cast<int *>(smem + C::kOffMisc + 4);
   int *n_bad_s = reinterpret_cast<int *>(smem + C::kOffMisc + 12);
   Start *start_s = reinterpret_cast<Start *>(smem + C::kOffMisc + 16);
+  int *range_s = reinterpret_cast<int *>(smem + C::kOffMisc + 16 + sizeof(Start));  // [2], before the pipeline runs
   long long *sum_s = reinterpret_cast<long long *>(col_s);                    // [warps], before the pipeline runs
   int *bad_list = reinterpret_cast<int *>(sp);                                // [NT * kScanPer], before the pipeline runs
 
@@ -581,15 +582,42 @@ __global__ void __launch_bounds__(Cfg<KV8, RT>::kThreads, 1)
       if (w < warp) before += sum_s[w];
       all += sum_s[w];
     }
-    if (any_bad) {  // rows of bad sequences: zeros
+    if (any_bad) {
+      // Rows of bad sequences: zeros, in the rows that no sequence with good offsets has, since other CTAs
+      // write those.  Such a sequence before s ends at or before the largest offset up to s, one behind it
+      // begins at or behind the smallest from s + 1 on (offsets outside [0, total_q] are no good
+      // sequence's), so the rows between the two are only s's.
       const int nb = *n_bad_s;
       for (int b = 0; b < nb; ++b) {
         const int s = bad_list[b];
-        const int lo = max(ld_cg(a.cu_q + s), 0), hi = min(ld_cg(a.cu_q + s + 1), a.total_q);
+        if (tid == 0) {
+          range_s[0] = 0;
+          range_s[1] = a.total_q;
+        }
+        __syncthreads();
+        int lo = 0, hi = a.total_q;
+        if (ld_cg(a.cu_q + s) < hi && ld_cg(a.cu_q + s + 1) > 0)  // (else it has no rows in the batch)
+          for (int i = tid; i <= a.batch; i += NT) {
+            const int c = ld_cg(a.cu_q + i);
+            if (c < 0 || c > a.total_q) continue;
+            if (i <= s) lo = max(lo, c);
+            else hi = min(hi, c);
+          }
+        else hi = 0;
+        lo = __reduce_max_sync(0xffffffffu, lo);
+        hi = __reduce_min_sync(0xffffffffu, hi);
+        if (lane == 0) {
+          atomicMax(range_s, lo);
+          atomicMin(range_s + 1, hi);
+        }
+        __syncthreads();
+        lo = range_s[0];
+        hi = range_s[1];
         for (long long i = (long long)lo * kHeads * (kD / 8) + tid; i < (long long)hi * kHeads * (kD / 8); i += NT)
           reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(0, 0, 0, 0);
         if (a.lse != nullptr)
           for (long long i = (long long)lo * kHeads + tid; i < (long long)hi * kHeads; i += NT) a.lse[i] = -INFINITY;
+        __syncthreads();  // range_s is written again
       }
       __syncthreads();
       if (tid == 0) *n_bad_s = 0;

@@ -333,9 +333,12 @@ s5_status s5_append_kv_fp8(const s5_kv_desc *kv, const s5_index_desc *index, con
  *     fixed size); rows from cu_q[batch] on are left as they were.
  *   device faults (S5_ERR_DEVICE_BOUNDS): a sequence with ctx_lens < 0, row
  *     offsets that decrease or leave [0, total_q], or ctx_lens + new tokens
- *     above max_len gives zeros and lse = -inf in its rows (info = its first
- *     row); the tokens of a page id outside the pool take no part (info = a
- *     row that would read it).  Other rows are unaffected.
+ *     above max_len is not computed; zeros and lse = -inf go into its rows (info
+ *     = its first row), of wrong offsets into those rows only that lie at or
+ *     behind all earlier offsets and before all later ones (of those in [0,
+ *     total_q]).  The tokens of a page id outside the pool take no part (info = a
+ *     row that would read it).  Other rows are unaffected; rows that two sequences
+ *     claim (a wrong offset lies between theirs) hold values of either.
  *   max_q: sequences of up to max_q <= 4 new tokens read their cache once for
  *     all of them; with more, once per 4 tokens.
  *   limits: total_q * 64 <= 2^31 - 1, num_pages * 256 < 2^31
