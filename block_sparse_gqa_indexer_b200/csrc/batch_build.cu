@@ -174,7 +174,10 @@ __global__ void __launch_bounds__(kBThreads) build_batch_kernel(const BuildArgs 
     }
     // ---- rows ----
     if (a.slots != nullptr || a.positions != nullptr) {
-      for (int r = s_cu[0] + blockIdx.x * kBThreads + tid; r < s_cu[kBSeqs]; r += gridDim.x * kBThreads) {
+      // (unsigned: a row number may be next to 2^31, and the step behind the last row passes it)
+      const uint32_t end = (uint32_t)s_cu[kBSeqs], step = gridDim.x * kBThreads;
+      for (uint32_t u = (uint32_t)s_cu[0] + blockIdx.x * kBThreads + tid; u < end; u += step) {
+        const int r = (int)u;
         int lo = 0, hi = n;  // the last k with s_cu[k] <= r: the sequence that has row r
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;

@@ -401,7 +401,8 @@ typedef struct {
  * A request may be in a batch once; page_table and req_pages must not overlap
  * (S5_ERR_INVALID_ARG).  slots of a page id above 2^25 - 2 (64 * page past 32
  * bits) are -1.
- * Limits: at most 65,535 sequences, max_pages <= 2^20 (S5_ERR_UNSUPPORTED). */
+ * Limits: at most 65,535 sequences, max_pages <= 2^20 (S5_ERR_UNSUPPORTED);
+ * total_q up to 2^31 - 1. */
 s5_status s5_build_batch(const s5_request_desc *requests, const int32_t *req_ids, const int32_t *new_lens,
                          const s5_batch_desc *batch, int32_t *slots, int32_t *positions, int32_t *pages_used,
                          void *workspace, size_t workspace_bytes, s5_stream_t stream);
