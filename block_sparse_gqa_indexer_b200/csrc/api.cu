@@ -31,6 +31,7 @@ static_assert((long long)kSeg * kMaxSeg >= S5_MAX_LEN / S5_BLOCK_SIZE, "segments
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
 // Longest history of any row: a query at t < max_len has c = t / 8 <= (max_len - 1) / 8 blocks.
 int max_blocks(const s5_batch_desc *b) {
@@ -370,6 +371,8 @@ s5_status attn_common(int mode, const s5_kv_desc *kv, const s5_batch_desc *b, co
   const int bpr = (mode == kModeSparse) ? sparse_blocks_per_row(topk) : swa_blocks_per_row(b, window);
   const AttnWs w = attn_ws(b, bpr, device_slots());
   if (ws_bytes < w.end) return S5_ERR_WORKSPACE;
+  // (the kernels read partial results 16 bytes at a time, and a 64-bit word of the header in any case)
+  if (!(w.n_split > 1 ? aligned16(ws) : aligned8(ws))) return S5_ERR_INVALID_ARG;
   CUtensorMap tk, tv;
   if (kv8) {
     if (!make_kv8_map(&tk, kv->k_pool, kv->num_pages) || !make_kv8_map(&tv, kv->v_pool, kv->num_pages))
@@ -411,6 +414,7 @@ s5_status attn_common(int mode, const s5_kv_desc *kv, const s5_batch_desc *b, co
     // kernel below skips the rows those tiles computed
     const TileWs tw = tile_ws(b, topk, device_slots() / kCtasPerSm, false, w.end);
     if (ws_bytes < tw.end) return S5_ERR_WORKSPACE;
+    if (tw.n_split > 1 && !aligned16(ws)) return S5_ERR_INVALID_ARG;
     CUtensorMap tpk, tpv;
     if (!make_kv_plane_map(&tpk, kv->k_pool, kv->num_pages) || !make_kv_plane_map(&tpv, kv->v_pool, kv->num_pages))
       return S5_ERR_CUDA;
@@ -534,6 +538,7 @@ s5_status dense_common(const s5_kv_desc *kv, const s5_batch_desc *b, const void 
   if (ws == nullptr) return S5_ERR_WORKSPACE;
   if (b->total_q == 0) return S5_OK;
   if (q == nullptr || out == nullptr || !aligned16(q) || !aligned16(out)) return S5_ERR_INVALID_ARG;
+  if (!aligned16(ws)) return S5_ERR_INVALID_ARG;
   const DenseWs w = dense_ws(b, device_slots() / kCtasPerSm);
   if (ws_bytes < w.end) return S5_ERR_WORKSPACE;
   uint8_t *wsb = static_cast<uint8_t *>(ws);
@@ -579,7 +584,7 @@ s5_status index_common(const s5_index_desc *index, const s5_batch_desc *batch, c
   if (topk < 1 || topk > kMaxTopk) return S5_ERR_INVALID_ARG;
   if (workspace == nullptr) return S5_ERR_WORKSPACE;
   if (batch->total_q == 0) return S5_OK;
-  if (q_index == nullptr || sel == nullptr || sel_count == nullptr || !aligned16(q_index))
+  if (q_index == nullptr || sel == nullptr || sel_count == nullptr || !aligned16(q_index) || !aligned16(workspace))
     return S5_ERR_INVALID_ARG;
   if (batch->batch > kMaxGridYZ) return S5_ERR_UNSUPPORTED;  // sequences index grid.y / grid.z
   const long long rows = (long long)batch->total_q * groups;

@@ -229,6 +229,7 @@ extern "C" s5_status s5_build_batch(const s5_request_desc *requests, const int32
     if (t0 < r1 && r0 < t1) return S5_ERR_INVALID_ARG;
   }
   if (workspace == nullptr || workspace_bytes < S5_WS_FIXED_BYTES) return S5_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 3u) != 0) return S5_ERR_INVALID_ARG;  // the error record's words
 
   BuildArgs a{};
   a.req_pages = requests->req_pages;

@@ -169,6 +169,7 @@ s5_status append_common(const s5_kv_desc *kv, const s5_index_desc *index, const 
   }
   if (workspace == nullptr || workspace_bytes < S5_WS_FIXED_BYTES) return S5_ERR_WORKSPACE;
   if (batch->total_q == 0) return S5_OK;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 3u) != 0) return S5_ERR_INVALID_ARG;  // the error record's words
   if (k_new == nullptr || v_new == nullptr || !aligned16(k_new) || !aligned16(v_new)) return S5_ERR_INVALID_ARG;
   if (index != nullptr && (key_new == nullptr || !aligned16(key_new))) return S5_ERR_INVALID_ARG;
 

@@ -127,7 +127,9 @@ typedef struct {
  * attention partition counters: zero them once before first use (or call
  * s5_reset_device_error); every call leaves the counters at zero again.  The
  * rest is per-call scratch with no state between calls.  Calls that share a
- * workspace must be ordered (one stream). */
+ * workspace must be ordered (one stream).  A workspace begins on a 16-byte
+ * boundary; the calls refuse one that their kernels could not use
+ * (S5_ERR_INVALID_ARG; those that use its error record alone take 4 bytes). */
 #define S5_WS_FIXED_BYTES (256 + 16384)
 /* Test hook for the bounded waits (not for normal use): a nonzero unsigned
  * 64-bit count of nanoseconds stored at this byte offset of a workspace makes
