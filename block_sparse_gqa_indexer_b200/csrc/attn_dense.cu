@@ -141,18 +141,36 @@ struct Seq {
   bool bad;
 };
 
-__device__ __forceinline__ Seq load_seq(const DenseArgs &a, int s) {
+__device__ __forceinline__ Seq load_seq(const int32_t *cu_q, const int32_t *ctx_lens, int total_q, int max_len, int s) {
   Seq q;
-  q.lo = ld_cg(a.cu_q + s);
-  const int hi = ld_cg(a.cu_q + s + 1);
-  q.ctx = ld_cg(a.ctx_lens + s);
-  q.bad = q.lo < 0 || hi < q.lo || hi > a.total_q;
+  q.lo = ld_cg(cu_q + s);
+  const int hi = ld_cg(cu_q + s + 1);
+  q.ctx = ld_cg(ctx_lens + s);
+  q.bad = q.lo < 0 || hi < q.lo || hi > total_q;
   q.n = q.bad ? 0 : hi - q.lo;
-  if (q.n > 0 && (q.ctx < 0 || q.ctx > a.max_len - q.n)) {
+  if (q.n > 0 && (q.ctx < 0 || q.ctx > max_len - q.n)) {
     q.bad = true;
     q.n = 0;
   }
   return q;
+}
+__device__ __forceinline__ Seq load_seq(const DenseArgs &a, int s) {
+  return load_seq(a.cu_q, a.ctx_lens, a.total_q, a.max_len, s);
+}
+
+// The first sequence from s on that has rows (batch: none).  The warp looks at 32 at a time, a lane each: one
+// after the other they are dependent reads of L2, and a call of 18 us took 44 with 100 sequences without
+// rows between two with rows (padded places of a batch), 757 with 3,000; 20 and 51 this way.  (A call for the
+// same reason as fill_bad: inlined, one-byte calls took up to 9% longer.)
+__device__ __noinline__ int next_live(const int32_t *cu_q, const int32_t *ctx_lens, int batch, int total_q, int max_len,
+                                      int s) {
+  const int lane = threadIdx.x & 31;
+  for (; s < batch; s += 32) {
+    const uint32_t live =
+        __ballot_sync(0xffffffffu, lane < batch - s && load_seq(cu_q, ctx_lens, total_q, max_len, s + lane).n > 0);
+    if (live != 0) return s + __ffs(live) - 1;
+  }
+  return batch;
 }
 
 // Units of the first m tiles, full ones: a tile counts its pages and, before them, START units for
@@ -227,7 +245,10 @@ struct Walk {
       if (++g == kKv) {
         g = 0;
         q.n = 0;
-        while (rem > 0 && q.n == 0 && ++s < a.batch) q = load_seq(a, s);
+        while (rem > 0 && q.n == 0 && ++s < a.batch) {
+          q = load_seq(a, s);
+          if (q.n == 0) s = next_live(a.cu_q, a.ctx_lens, a.batch, a.total_q, a.max_len, s + 1) - 1;
+        }
         if (q.n == 0) rem = 0;
       }
     }
