@@ -487,6 +487,10 @@ struct DenseWs {
   int tile_rows, n_ctas;
 };
 
+// Every CTA reads every sequence's lengths (its place in 32-bit numbers), and for a bad sequence all
+// offsets once more, so the batch is bounded: by about as many sequences as the GPU has memory for pages.
+constexpr int kDenseMaxBatch = 1 << 20;
+
 // Batches of sequences up to this long do not split tiles over CTAs, which saves the joining kernel.
 // Measured, split against whole, bf16: 8 requests of 400 tokens 14.6 / 12.2 us, of 700 16.6 / 13.0, of 1,000
 // 15.5 / 15.5; 1 request of 400 13.0 / 11.8, of 700 11.5 / 12.6, of 1,000 12.3 / 15.1.
@@ -535,6 +539,7 @@ s5_status dense_common(const s5_kv_desc *kv, const s5_batch_desc *b, const void 
   if (!std::isfinite(sm_scale)) return S5_ERR_INVALID_ARG;
   if (kv8 && (!std::isfinite(k_scale) || !std::isfinite(v_scale) || !std::isfinite(sm_scale * k_scale)))
     return S5_ERR_INVALID_ARG;
+  if (b->batch > kDenseMaxBatch) return S5_ERR_UNSUPPORTED;
   if (ws == nullptr) return S5_ERR_WORKSPACE;
   if (b->total_q == 0) return S5_OK;
   if (q == nullptr || out == nullptr || !aligned16(q) || !aligned16(out)) return S5_ERR_INVALID_ARG;

@@ -343,7 +343,7 @@ s5_status s5_append_kv_fp8(const s5_kv_desc *kv, const s5_index_desc *index, con
  *     claim (a wrong offset lies between theirs) hold values of either.
  *   max_q: sequences of up to max_q <= 4 new tokens read their cache once for
  *     all of them; with more, once per 4 tokens.
- *   limits: total_q * 64 <= 2^31 - 1, num_pages * 256 < 2^31
+ *   limits: at most 2^20 sequences, total_q * 64 <= 2^31 - 1, num_pages * 256 < 2^31
  *     (S5_ERR_UNSUPPORTED otherwise).
  * The workspace is the one of s5_workspace_size_dense (which also covers every
  * call that s5_workspace_size covers); its contents besides the error record
