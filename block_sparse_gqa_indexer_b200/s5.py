@@ -157,6 +157,10 @@ class Batch:
         _need(ctx_lens, torch.int32, "ctx_lens")
         _need(cu_q, torch.int32, "cu_q")
         assert page_table.dim() == 2 and cu_q.numel() == ctx_lens.numel() + 1
+        if page_table.shape[0] < ctx_lens.numel():
+            raise ValueError(f"page_table has {page_table.shape[0]} rows for {ctx_lens.numel()} sequences")
+        if not page_table.device == ctx_lens.device == cu_q.device:
+            raise ValueError(f"page_table, ctx_lens and cu_q are on {page_table.device}, {ctx_lens.device} and {cu_q.device}")
         self.page_table, self.ctx_lens, self.cu_q = page_table, ctx_lens, cu_q
         self.total_q, self.max_q, self.max_len = int(total_q), int(max_q), int(max_len)
         self.desc = BatchDesc(page_table.data_ptr(), ctx_lens.data_ptr(), cu_q.data_ptr(), ctx_lens.numel(),
