@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kBThreads) build_batch_kernel(const BuildArgs 
       int32_t *req = a.req_pages + (size_t)max(s_id[k], 0) * a.req_stride;
       int32_t *dst = a.page_table + (size_t)(s0 + k) * a.max_pages;
       constexpr int W = VEC ? 4 : 1, N = kBCols / (32 * W);  // columns of a piece, pieces of a lane
-      int32_t v[N][W];
+      alignas(16) int32_t v[N][W];  // (pieces of W = 4 go in and out as one int4)
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int c = c0 + (i * 32 + lane) * W;
