@@ -395,6 +395,11 @@ typedef struct {
  *                on are left as they were
  *   pages_used   device int32 [1], or NULL
  *   workspace    at least S5_WS_FIXED_BYTES; only its error record is used
+ * The pages come from the front of free_pages at every call: a step replayed
+ * without the host moves the pages left to the front of the array by itself,
+ * behind this call (an entry that is not a page, -1, is handed on as it is).
+ * Rows from cu_q[batch] on belong to no sequence: dense attention leaves them,
+ * the cache appends record them as faults.
  * Device faults (S5_ERR_DEVICE_BOUNDS, info = the sequence): a request id
  * outside [-1, num_reqs), a negative length, ctx + new above S5_MAX_LEN or more
  * pages than max_pages or req_stride make that sequence an empty one; a page
