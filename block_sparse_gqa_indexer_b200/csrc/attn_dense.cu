@@ -1227,10 +1227,11 @@ __global__ void __launch_bounds__(Cfg<KV8, RT>::kThreads, 1)
 // Work items: of a tile of at most kFewParts parts four (row, head) pairs, a warp each; of a tile of more
 // parts one pair, whose parts the CTA's warps share (warp w takes parts w, w + 4, ...; their sums are
 // added in warp order).  Few parts come with many tiles and many parts with few tiles, so either way the
-// SMs have enough items and a few rounds of loads end each.  About 5 us behind the first kernel, for 4
+// SMs have enough items and a few rounds of loads end each.  4 to 5 us behind the first kernel, for 4
 // tiles of 37 parts as for 130 of 2 or 3; latency-bound (records, then references, sums and parts, one
-// round trip each, and the launch).
-constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32, kJoinCtasPerSm = 6;
+// round trip each, and the launch).  Four CTAs per SM: six hold a thread to 80 registers, which spills 100
+// bytes and makes the calls 0.4 to 0.9 us longer (1 x 1,000 tokens 10.7 against 10.3 us).
+constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32, kJoinCtasPerSm = 4;
 constexpr int kFewParts = 4, kMaxCtas = 256;
 static_assert(kMaxCtas == 2 * kJoinThreads, "two records per thread");
 
