@@ -491,10 +491,21 @@ struct DenseWs {
 // offsets once more, so the batch is bounded: by about as many sequences as the GPU has memory for pages.
 constexpr int kDenseMaxBatch = 1 << 20;
 
-// Batches of sequences up to this long do not split tiles over CTAs, which saves the joining kernel.
-// Measured, split against whole, bf16: 8 requests of 400 tokens 14.6 / 12.2 us, of 700 16.6 / 13.0, of 1,000
-// 15.5 / 15.5; 1 request of 400 13.0 / 11.8, of 700 11.5 / 12.6, of 1,000 12.3 / 15.1.
-constexpr int kDenseWholeLen = 768;
+// Batches of sequences up to this long do not split tiles over CTAs, which saves the joining kernel and lengthens
+// the longest share.  Measured, split / whole in us (GPU time, sequences of equal length; columns: 1 and 4 new
+// tokens in bf16, 1 and 4 in one byte):
+//                  256 tokens                                   400 tokens
+//    1 sequence    9.2/8.2    12.9/12.1  8.9/7.7    13.0/11.8   10.3/10.9  13.3/15.4  9.5/9.9    13.4/14.2
+//    4             9.8/8.5    14.5/12.9  9.5/8.0    13.7/12.4   11.4/11.2  15.1/15.9  10.7/10.3  15.3/14.6
+//    8             10.9/9.2   15.9/13.3  10.1/8.6   14.5/12.7   12.6/11.8  16.9/16.2  12.1/10.8  16.6/14.8
+//   64             18.3/16.4  27.6/25.2  17.2/15.1  25.1/22.7   27.0/23.2  38.0/31.6  24.4/19.6  35.4/27.7
+//                  700                                          1,000
+//    1             10.1/11.9  13.9/17.9  10.1/11.2  14.2/16.1   10.7/14.6  14.7/21.7  10.3/13.5  14.3/18.9
+//    4             12.2/12.3  16.5/18.4  11.5/11.7  15.1/16.4   13.0/15.1  17.9/22.0  11.9/13.9  15.5/19.1
+//    8             14.5/12.8  17.0/18.8  11.7/12.0  16.6/16.8   15.0/15.6  19.0/22.5  13.0/14.2  18.2/19.2
+//   64             32.0/27.8  44.0/37.7  27.8/22.4  39.7/31.9   40.6/37.2  51.4/46.2  31.9/27.2  44.9/37.0
+// max_len is what the host knows: a batch made for longer sequences splits.
+constexpr int kDenseWholeLen = 768, kDenseWholeLenFew = 256, kDenseFew = 8;  // (... of fewer than kDenseFew sequences)
 
 // One persistent CTA per SM, fewer when the batch cannot have that many page
 // units (pages times KV groups, per tile of rows).
@@ -566,7 +577,7 @@ s5_status dense_common(const s5_kv_desc *kv, const s5_batch_desc *b, const void 
   a.tile_rows = w.tile_rows;
   a.reread = b->max_q > w.tile_rows ? 1 : 0;
   a.n_ctas = w.n_ctas;
-  a.whole = b->max_len <= kDenseWholeLen ? 1 : 0;
+  a.whole = b->max_len <= (b->batch < kDenseFew ? kDenseWholeLenFew : kDenseWholeLen) ? 1 : 0;
   a.out = out;
   a.lse = lse;
   a.part_o = reinterpret_cast<float *>(wsb + w.part_o);
