@@ -10,7 +10,9 @@
 // Bound: HBM.  A cached token costs 3 KB (bf16) for 16 FLOPs per byte and
 // query row, far below the tensor cores' ratio even for the 4 rows of a tile, so
 // the aim is a full stream of pages on every SM: 32 requests x 131,072 bf16 tokens
-// take 1.80 ms = 7.2 TB/s, 64 x 49,000 one-byte tokens 0.70 to 0.76 ms = 6.7 to 6.2.
+// take 1.81 to 1.85 ms = 7.1 to 7.0 TB/s, 64 x 30,000 to 65,536 one-byte tokens 0.71 ms = 6.6 TB/s in a replayed graph
+// and 0.77 to 0.80 ms in calls in sequence with other inputs (the power limit holds the SM clock at 1.4 to 1.8 GHz,
+// and times follow it).
 //
 // Split.  The work is a list of page units: sequences in order, in each its KV
 // groups, in each group its tiles of `tile_rows` query rows, in each tile the
@@ -22,7 +24,7 @@
 // begins, and there is nothing to join.
 // (Joined by the last CTA to arrive, in two levels, a tile of 37 parts took 14 us,
 // of 4 rows 21 us: two counters' round trips, and the parts read by one SM.  The
-// second kernel takes about 5 us.)
+// second kernel takes 4 to 5 us.)
 //
 // One CTA works in chunks of two pages (128 tokens): a warp streams K and another
 // V, one TMA copy per page and KV group, through rings in shared memory; one warp
@@ -63,7 +65,7 @@ template <bool KV8, int RT>
 struct Cfg {
   static constexpr int kPairs = RT * kHpg;            // (row, head) pairs of a tile: columns of S^T and O^T
   // Softmax warps: 4, a thread per token, or (2 and 4 rows) 8, two threads per token with half of the
-  // columns each (one-byte KV, 16 x 16,384 tokens, 2 rows: 80 against 73 us; 4 rows: 121 against 93 us).
+  // columns each (one-byte KV, 16 x 16,384 tokens, 2 rows: 80 against 73 us; 4 rows: 121 against 86 to 93 us).
   static constexpr int kSoftWarps = RT >= 2 ? 8 : 4, kSoft = 32 * kSoftWarps, kThreads = kSoft + 128;
   static constexpr int kHalves = kSoftWarps / 4, kCols = kPairs / kHalves;  // threads per token, their columns
   static constexpr int kWarpK = kSoftWarps, kWarpV = kWarpK + 1, kWarpS = kWarpK + 2, kWarpPv = kWarpK + 3;

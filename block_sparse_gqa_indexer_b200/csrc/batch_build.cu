@@ -13,8 +13,8 @@
 // at a time, 4 per thread, 12 bytes read per sequence, in L2 after the first
 // CTA) instead of waiting for another CTA's; then its warps take 256 columns of a
 // table row at a time, all their loads in flight together, and its threads a new
-// token each.  Measured (replayed graph): 3.3 us for 8 requests, 4.4 us for 16
-// prefill chunks of up to 2,048 tokens, 7.0 us for 1,024 requests of up to 131,072
+// token each.  Measured (replayed graph): 3.3 us for 8 requests, 4.6 us for 16
+// prefill chunks of up to 2,048 tokens, 7.1 us for 1,024 requests of up to 131,072
 // tokens (12.6 MB), where a table entry per thread and step took 9.5 us.
 #include <cuda_runtime.h>
 

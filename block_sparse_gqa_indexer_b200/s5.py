@@ -449,7 +449,9 @@ def s5_build_batch(req_pages, req_ids, new_lens, free_pages, batch: Batch, slots
     ``pages_used`` [1] (each may be None), from the requests' pages ``req_pages``
     [num_reqs][stride] (which receives the pages taken from ``free_pages``), the
     request of each sequence ``req_ids`` [batch] (-1: empty), ``batch.ctx_lens``
-    and ``new_lens`` [batch].  ``batch.total_q`` is the sum of the new tokens."""
+    and ``new_lens`` [batch].  ``batch.total_q`` is the sum of the new tokens.
+    ``ws``: ``S5_WS_FIXED_BYTES`` zeroed bytes are enough (``new_workspace`` sizes
+    for the indexer's scores too, which many new tokens make large)."""
     if req_pages is None or req_ids is None or new_lens is None or free_pages is None or ws is None:
         raise TypeError("req_pages, req_ids, new_lens, free_pages and ws must be CUDA tensors")
     pages, ids, new, free, sl, pos, used, wp, _ = _ptrs(

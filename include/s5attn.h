@@ -323,9 +323,11 @@ s5_status s5_append_kv_fp8(const s5_kv_desc *kv, const s5_index_desc *index, con
  *   out = sum_{j <= t} softmax_j(sm_scale * q[r][h] . K[j][g]) V[j][g]
  *   lse = log sum_{j <= t} exp(sm_scale * q[r][h] . K[j][g])   (may be NULL)
  * A sequence's cache is split over the SMs in equal shares (from the device's
- * lengths, so ragged batches balance too; the shares and with them the results
- * depend on the lengths and the GPU's SM count only) and the parts are joined by
- * their log-sum-exp.  K or V values at positions > t never reach row r, not
+ * lengths, so ragged batches balance too) and the parts are joined by their
+ * log-sum-exp.  The last bits of a row's result depend on how the work is divided,
+ * that is on the batch's lengths, batch, total_q, max_q, max_len and the GPU's SM
+ * count, and for one-byte KV on the queries of the rows computed together with it
+ * (below); equal calls give equal bits.  K or V values at positions > t never reach row r, not
  * even as infinities or NaN.  A V value at a position <= t that is not finite
  * makes its dimension of the row's 16 heads not finite (NaN or an infinity); a
  * score that is NaN or +inf makes its row and head not finite; a score of -inf
